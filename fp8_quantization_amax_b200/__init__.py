@@ -18,7 +18,8 @@ import torch
 
 __all__ = [
     "E4M3", "E5M2", "PER_TENSOR", "GROUP_1x128", "BLOCK_128x128",
-    "KV_PER_TENSOR", "KV_PER_HEAD", "KV_PER_HEAD_TOK128",
+    "KV_PER_TENSOR", "KV_PER_HEAD", "KV_PER_HEAD_TOK128", "KV_PER_TOKEN",
+    "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_SMOOTH", "ROPE_RAMP",
     "Fp8qError", "lib", "library_path", "device_status", "num_scales", "workspace_bytes", "kv_num_scales",
     "kv_workspace_bytes", "gemm_workspace_bytes", "scale_shape", "kv_scale_shape",
     "fp8_encode", "fp8_decode", "fp8_quantize", "fp8_dequantize", "fp8_kv_quantize",
@@ -28,11 +29,14 @@ __all__ = [
     "mx_blocked_scale_bytes", "fp8_quantize_mx_blocked", "fp8_gemm_mx", "fp8_pack_b_tiles",
     "fp8_gemm_blockscaled_packed", "fp8_scale_histogram", "fp8_count_underflow", "fp8_quantize_many",
     "selftest_wait_timeout", "fp8_gemm_blockscaled_to_fp8", "check_decode_split", "check_tile_walk",
+    "pages_workspace_bytes", "fp8_kv_pages_update", "rope_turns", "fp8_kv_append", "attention_workspace_bytes",
+    "check_attention_split", "fp8_attention_paged", "kv_page_scale_shape",
 ]
 
 E4M3, E5M2 = 0, 1
 PER_TENSOR, GROUP_1x128, BLOCK_128x128 = 0, 1, 2
-KV_PER_TENSOR, KV_PER_HEAD, KV_PER_HEAD_TOK128 = 0, 1, 2
+KV_PER_TENSOR, KV_PER_HEAD, KV_PER_HEAD_TOK128, KV_PER_TOKEN = 0, 1, 2, 3
+ROPE_PLAIN, ROPE_LINEAR, ROPE_SMOOTH, ROPE_RAMP = 0, 1, 2, 3
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfp8q.so")
@@ -44,6 +48,15 @@ class _QuantTensor(ctypes.Structure):
     """fp8q_quant_tensor of include/fp8q.h."""
     _fields_ = [("x", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("g", ctypes.c_int),
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _KvPages(ctypes.Structure):
+    """fp8q_kv_pages of include/fp8q.h."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("f", ctypes.c_int),
+                ("g", ctypes.c_int)]
 
 
 class Fp8qError(RuntimeError):
@@ -107,6 +120,20 @@ def lib() -> ctypes.CDLL:
             L.fp8q_linear_fused_workspace_bytes.argtypes = [i64, i64]
             L.fp8q_linear_fused_workspace_bytes.restype = sz
             L.fp8_linear_dynamic_fused.argtypes = [vp, i64, i64, i64, vp, vp, i32, vp, vp, sz, vp]
+            f32, f64, pages = ctypes.c_float, ctypes.c_double, ctypes.POINTER(_KvPages)
+            L.fp8q_pages_workspace_bytes.argtypes = [i64, i64]
+            L.fp8q_pages_workspace_bytes.restype = sz
+            L.fp8_kv_pages_update.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, i64, vp, vp, vp, vp, vp,
+                                              sz, vp]
+            L.fp8q_rope_turns.argtypes = [i64, f64, i32, f64, f64, f64, f64, vp, ctypes.POINTER(f32)]
+            L.fp8_kv_append.argtypes = [pages, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, f32, vp, vp,
+                                        f32, vp, i64, vp]
+            L.fp8q_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+            L.fp8q_attention_workspace_bytes.restype = sz
+            L.fp8q_check_attention_split.argtypes = [vp, i64, i64, i64, i32]
+            L.fp8q_check_attention_split.restype = i32
+            L.fp8_attention_paged.argtypes = [pages, vp, i64, i64, vp, i64, i64, vp, f32, i64, i64, vp, i64, vp, vp,
+                                              sz, vp]
             L.fp8_encode.argtypes = [vp, i64, i32, vp, vp]
             L.fp8_decode.argtypes = [vp, i64, i32, vp, vp]
             L.fp8_quantize.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp, sz, vp]
@@ -123,7 +150,8 @@ def lib() -> ctypes.CDLL:
                        "fp8_quantize_mx", "fp8_dequantize_mx",
                        "fp8_quantize_mx_blocked", "fp8_gemm_mx", "fp8_pack_b_tiles",
                        "fp8_gemm_blockscaled_packed", "fp8_scale_histogram", "fp8_count_underflow",
-                       "fp8_quantize_many"):
+                       "fp8_quantize_many", "fp8_kv_pages_update", "fp8q_rope_turns", "fp8_kv_append",
+                       "fp8_attention_paged"):
                 getattr(L, fn).restype = i32
             _lib = L
     return _lib
@@ -717,3 +745,254 @@ def fp8_dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, fmt: int = E4M3
     _check("fp8_dequantize_mx", lib().fp8_dequantize_mx(_ptr(codes), _ptr(scales), rows, cols, fmt, _ptr(out),
                                                        _stream(codes.device)))
     return out
+
+
+# ------------------------------------------------------------------ paged KV cache
+
+def _paged_on(dev: int, *tensors) -> None:
+    """Every given tensor lies on CUDA device `dev`."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors of a call must be on one CUDA device (this library has no CPU path)")
+
+
+def _expect(t, name: str, dtype, shape=None) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _call_on(dev: int, fn: str, *args) -> None:
+    """Call the library with `dev` current, on its current stream (the last argument)."""
+    if torch.cuda.current_device() == dev:
+        _check(fn, getattr(lib(), fn)(*args, _raw_stream_of(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn, getattr(lib(), fn)(*args, _raw_stream_of(dev)))
+
+
+def _raw_stream_of(dev: int) -> int:
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def kv_page_scale_shape(num_pages: int, page_size: int, heads: int, gran: int) -> tuple:
+    """Shape of the K (and V) scales of a paged cache: see fp8q_kv_pages in include/fp8q.h."""
+    if gran == KV_PER_TOKEN:
+        return (heads, num_pages * page_size)
+    return kv_scale_shape(num_pages * page_size, heads, gran)
+
+
+def _pages_struct(k_cache, v_cache, k_scales, v_scales, fmt: int, gran: int) -> _KvPages:
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name} must be torch.uint8, got {t.dtype}")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must both be [num_pages][page_size][heads][head_dim] with equal strides")
+    n, size, heads, d = k_cache.shape
+    page, token, head, one = k_cache.stride()
+    if one != 1:
+        raise ValueError("k_cache and v_cache must be contiguous along head_dim")
+    shape = kv_page_scale_shape(n, size, heads, gran)
+    _expect(k_scales, "k_scales", torch.float32, shape)
+    _expect(v_scales, "v_scales", torch.float32, shape)
+    # strides of single-entry dimensions are not used
+    return _KvPages(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), n, size, heads, d,
+                    page if n > 1 else 0, token if size > 1 else 0, head if heads > 1 else 0, fmt, gran)
+
+
+def _heads_of(x: torch.Tensor, name: str) -> int:
+    """Token stride of bf16 [tokens][heads][head_dim] whose heads are contiguous within a token."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [tokens][heads][head_dim]")
+    token, head, one = x.stride()
+    if (one != 1 and x.shape[2] > 1) or (head != x.shape[2] and x.shape[1] > 1):
+        raise ValueError(f"{name} must be contiguous within a token")
+    return token if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def pages_workspace_bytes(batch: int, max_tokens: int) -> int:
+    return int(lib().fp8q_pages_workspace_bytes(batch, max_tokens))
+
+
+def fp8_kv_pages_update(block_table: torch.Tensor, lens: torch.Tensor, added: torch.Tensor, free_pages: torch.Tensor,
+                        free_count: torch.Tensor, page_size: int, max_tokens: int | None = None,
+                        slots: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                        offsets: torch.Tensor | None = None, served: torch.Tensor | None = None,
+                        lens_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
+                        ws: torch.Tensor | None = None):
+    """The page bookkeeping of one serving step, on the device.  block_table int32 [batch][max_pages]
+    and free_pages int32 [num_pages] are updated in place, lens int32 [batch] and free_count int32 [1]
+    too unless lens_out / free_count_out are given.  added int32 [batch]: new tokens of each request,
+    negative for one that ends.  -> (slots int64 [max_tokens], positions int32 [max_tokens], offsets
+    int32 [batch + 1], served int32 [batch], lens_out, free_count_out); max_tokens, an upper bound of
+    the added tokens known on the host, may be left out when slots is given."""
+    i32 = torch.int32
+    _expect(block_table, "block_table", i32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [batch][max_pages]")
+    batch, max_pages = block_table.shape
+    _expect(lens, "lens", i32, (batch,))
+    _expect(added, "added", i32, (batch,))
+    _expect(free_pages, "free_pages", i32)
+    _expect(free_count, "free_count", i32, (1,))
+    if max_tokens is None:
+        if slots is None:
+            raise ValueError("max_tokens or slots must be given")
+        max_tokens = slots.numel()
+    dev = block_table.get_device()
+    if slots is None:
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=block_table.device)
+    if positions is None:
+        positions = torch.empty(max_tokens, dtype=i32, device=block_table.device)
+    if offsets is None:
+        offsets = torch.empty(batch + 1, dtype=i32, device=block_table.device)
+    if served is None:
+        served = torch.empty(batch, dtype=i32, device=block_table.device)
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _expect(slots, "slots", torch.int64, (max_tokens,))
+    _expect(positions, "positions", i32, (max_tokens,))
+    _expect(offsets, "offsets", i32, (batch + 1,))
+    _expect(served, "served", i32, (batch,))
+    _expect(lens_out, "lens_out", i32, (batch,))
+    _expect(free_count_out, "free_count_out", i32, (1,))
+    _paged_on(dev, block_table, lens, added, free_pages, free_count, slots, positions, offsets, served, lens_out,
+              free_count_out, ws)
+    if dev < 0:
+        raise ValueError("block_table must be a CUDA tensor (this library has no CPU path)")
+    ws = _workspace(pages_workspace_bytes(batch, max_tokens), block_table.device, ws)
+    _call_on(dev, "fp8_kv_pages_update", block_table.data_ptr(), batch, max_pages, page_size, lens.data_ptr(),
+             added.data_ptr(), lens_out.data_ptr(), free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
+             free_count_out.data_ptr(), max_tokens, slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
+             served.data_ptr(), None if ws is None else ws.data_ptr(),
+             0 if ws is None else ws.numel() * ws.element_size())
+    return slots, positions, offsets, served, lens_out, free_count_out
+
+
+def rope_turns(rot_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
+               original_len: float = 8192.0, low: float = 1.0, high: float = 4.0, device=None):
+    """Rotary frequencies for fp8_kv_append: (turns int64 [rot_dim / 2] holding 64-bit fractions of a
+    turn per position, gain).  Host only; the tensor is made on `device`.  See fp8q_rope_turns in
+    include/fp8q.h for the kinds."""
+    host = torch.empty(rot_dim // 2 if rot_dim > 0 else 0, dtype=torch.int64)
+    gain = ctypes.c_float()
+    _check("fp8q_rope_turns", lib().fp8q_rope_turns(rot_dim, base, kind, factor, original_len, low, high,
+                                                   host.data_ptr() or None, ctypes.byref(gain)))
+    return (host if device is None else host.to(device)), float(gain.value)
+
+
+def fp8_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, fmt: int = E4M3,
+                  gran: int = KV_PER_HEAD, positions: torch.Tensor | None = None, turns: torch.Tensor | None = None,
+                  interleaved: bool = False, gain: float = 1.0, q_weight: torch.Tensor | None = None,
+                  k_weight: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None):
+    """New tokens into a paged FP8 cache: per-head RMS norm (with weights bf16 [head_dim]) and rotation
+    (with positions int32 [tokens] and turns of rope_turns) of q and k, k and v quantized into their
+    slots (int64 [tokens], negative: padding); -> q_out, bf16 [tokens][q_heads][head_dim] (may be q).
+    q, k, v: bf16 [tokens][heads][head_dim], contiguous within a token.  KV_PER_TENSOR and KV_PER_HEAD
+    read the scales, KV_PER_TOKEN writes them."""
+    ks, vs = _heads_of(k, "k"), _heads_of(v, "v")
+    cache = _pages_struct(k_cache, v_cache, k_scales, v_scales, fmt, gran)
+    tokens, heads, d = k.shape
+    if v.shape != k.shape or heads != cache.heads or d != cache.head_dim:
+        raise ValueError("k and v must both be [tokens][heads][head_dim] of the cache")
+    _expect(slots, "slots", torch.int64, (tokens,))
+    q_heads, qs, qos = 0, 0, 0
+    if q is not None:
+        qs = _heads_of(q, "q")
+        if q.shape[0] != tokens or q.shape[2] != d:
+            raise ValueError("q must be [tokens][q_heads][head_dim]")
+        q_heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        qos = _heads_of(q_out, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = 0
+    if turns is not None:
+        _expect(turns, "turns", torch.int64)
+        rot = 2 * turns.numel()
+        if positions is None and rot:
+            raise ValueError("turns without positions")
+    if positions is not None:
+        _expect(positions, "positions", torch.int32, (tokens,))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _expect(w, name, torch.bfloat16, (d,))
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("k must be a CUDA tensor (this library has no CPU path)")
+    _paged_on(dev, q, v, slots, k_cache, v_cache, k_scales, v_scales, positions, turns, q_weight, k_weight, q_out)
+    _call_on(dev, "fp8_kv_append", cache, None if q is None else q.data_ptr(), qs, q_heads, k.data_ptr(), ks,
+             v.data_ptr(), vs, tokens, slots.data_ptr(), None if positions is None else positions.data_ptr(),
+             None if turns is None else turns.data_ptr(), rot, 1 if interleaved else 0, gain,
+             None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+             None if q_out is None else q_out.data_ptr(), qos)
+    return q_out
+
+
+@functools.lru_cache(maxsize=1024)
+def attention_workspace_bytes(batch: int, max_tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of fp8_attention_paged; max_tokens = max_pages * page_size."""
+    return int(lib().fp8q_attention_workspace_bytes(batch, max_tokens, q_heads, kv_heads, head_dim))
+
+
+def check_attention_split(lens, window: int = 0, sinks: int = 0, workers: int = 148) -> int:
+    """Host-only check of the paged attention's division of work: 0 when every visible token of the
+    requests (a sequence of lengths) is read exactly once.  See fp8q_check_attention_split."""
+    arr = (ctypes.c_int32 * max(1, len(lens)))(*lens)
+    return int(lib().fp8q_check_attention_split(arr, len(lens), window, sinks, workers))
+
+
+def fp8_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                        v_scales: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, fmt: int = E4M3,
+                        gran: int = KV_PER_HEAD, scale: float | None = None, window: int = 0, sinks: int = 0,
+                        out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        ws: torch.Tensor | None = None):
+    """Attention of one new token per request over its pages: q bf16 [batch][q_heads][head_dim] ->
+    (out bf16 of the same shape, lse fp32 [batch][q_heads]).  block_table int32 [batch][max_pages], lens
+    int32 [batch] (the new token included).  window > 0: only the last `window` tokens and the first
+    `sinks` are visible.  scale: head_dim ** -0.5 when not given.  ws: scratch, allocated when not
+    given (so calls on different streams or in different graphs never share one)."""
+    qs = _heads_of(q, "q")
+    cache = _pages_struct(k_cache, v_cache, k_scales, v_scales, fmt, gran)
+    batch, q_heads, d = q.shape
+    heads = cache.heads
+    if d != cache.head_dim or q_heads == 0 or heads == 0 or q_heads % heads:
+        raise ValueError("q must be [batch][q_heads][head_dim] with q_heads a multiple of the cache's heads")
+    _expect(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be [batch][max_pages]")
+    _expect(lens, "lens", torch.int32, (batch,))
+    if out is None:
+        out = torch.empty((batch, q_heads, d), dtype=torch.bfloat16, device=q.device)
+    os_ = _heads_of(out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = torch.empty((batch, q_heads), dtype=torch.float32, device=q.device)
+    _expect(lse, "lse", torch.float32, (batch, q_heads))
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor (this library has no CPU path)")
+    _paged_on(dev, k_cache, v_cache, k_scales, v_scales, block_table, lens, out, lse, ws)
+    max_pages = block_table.shape[1]
+    nbytes = attention_workspace_bytes(batch, max_pages * cache.page_size, q_heads, heads, d)
+    ws = _workspace(nbytes, q.device, ws)
+    _call_on(dev, "fp8_attention_paged", cache, q.data_ptr(), qs, q_heads, block_table.data_ptr(), batch, max_pages,
+             lens.data_ptr(), d ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), os_, lse.data_ptr(),
+             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
+    return out, lse

@@ -1,0 +1,808 @@
+// Attention of one new token per request over a paged FP8 KV cache (fp8_attention_paged).
+//
+//   z_j = scale s_k(j) sum_d q_d K_jd,   o_d = sum_j 2^(z_j log2 e - m) s_v(j) V_jd / sum_j 2^(z_j log2 e - m)
+//
+// over the visible tokens j of a request, K and V the decoded codes, for each query head; `group`
+// query heads share a key-value head.  One pass over K and V with the running maximum m and sum
+// of the softmax.
+//
+// What bounds it: the codes, 2 heads head_dim bytes a token, are read once from HBM.  With a
+// group of 8 every byte meets 8 multiply-adds, 52 T a second at the memory's rate, above the fp32
+// pipes' 36 T: the products go to the tensor cores, m16n8k16 with f16 operands and fp32 sums.
+// Every code is exact in f16, a query (bf16) times a power of two of its row is as well, and only
+// the softmax weights are rounded to f16 (half a step is 2^-12 of a weight, below the output's
+// bf16 2^-9).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
+//
+//   S (query x token): A = q (rows g: query heads), B = K (columns: tokens)
+//   O^T (dim x query): A = V^T (rows: dims), B = P^T (columns: query heads)
+//
+// The result of S leaves each thread with the weights of head g = lane / 4 for tokens 2t, 2t + 1
+// (t = lane % 4), which is what B of the second product wants of it: no exchange between the two.
+// The sum's order over dims and the dims' order in O^T are free, so thread t reads 16 contiguous
+// bytes of a K row per 64 dims, and thread g head_dim / 8 contiguous bytes of a V row.
+//
+// Each warp streams the tokens of one key-value head on its own through a private ring of
+// 16-token stages (cp.async, no barrier between warps); the warps of a block take adjacent heads
+// of the same tokens, so a [token][head][dim] page is read in whole rows.  With fewer heads than
+// warps several warps take every second, third ... tile of a head and are joined in shared memory.
+//
+// All requests' tiles laid end to end are divided evenly over one wave of blocks (kv_pages.cuh), from
+// the lengths on the device: ragged batches and one long request fill the machine alike.  A
+// request whose tiles are shared leaves fp32 partial results, joined by a second launch in the
+// blocks' order, so results do not depend on timing.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "fp8q_device.cuh"
+#include "internal.h"
+#include "kv_pages.cuh"
+#include "sm100.cuh"
+
+namespace fp8q {
+namespace attn {
+
+constexpr int kWarps = 8;
+constexpr int kMinTiles = 4;
+constexpr int kStages = 3;
+constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = 32 * kJoinWarps;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Params {
+  KvPages c;
+  const uint16_t* q;
+  int64_t q_stride;          // elements from request to request
+  const int* table;
+  const int* lens;
+  int batch, max_pages, group;
+  int window, sinks;
+  float scale2;              // softmax scale times log2 e
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;
+  int vheads, row_tiles;     // (key-value head, tile of query rows) pairs; query-row tiles per head
+  int heads_per_block, phases;
+  int workers;               // gridDim.x of the first launch
+  int4* desc;                // per worker: the shared request that begins in its range
+  float* part;               // per (worker, first or last request, vhead): a warp's registers
+  uint32_t* err;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// 2^(a - b) with b = -inf standing for "nothing yet" (a is -inf too then)
+__device__ __forceinline__ float ex2_diff(float a, float b) { return b == -INFINITY ? 0.0f : ex2(a - b); }
+
+__device__ __forceinline__ int clamped_len(const Params& p, int b) {
+  const int n = __ldg(p.lens + b);
+  return (int)max((int64_t)0, min((int64_t)n, min((int64_t)p.max_pages * p.c.page_size, (int64_t)kMaxTokens)));
+}
+
+// Running softmax and product of one warp's query rows, as it lies in a thread's registers.
+// Row r = 8 n + lane / 4 has its maximum (base 2) and sum in m[n], l[n] (the four threads of a row
+// agree on m, and on l once reduced); o[n][i] holds dims VB g + 2 i (elements 0, 1) and
+// VB g + 2 i + 1 (elements 2, 3) of rows 8 n + 2 t and 8 n + 2 t + 1.
+template <int DP, int NH>
+struct State {
+  static constexpr int kDimTiles = DP / 16;
+  static constexpr int kFloats = NH * (4 * kDimTiles + 2);
+  float m[NH], l[NH], o[NH][kDimTiles][4];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kDimTiles; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
+    }
+  }
+  // multiply the rows of tile n by a factor that lives in the rows' own threads
+  __device__ __forceinline__ void scale_rows(int n, float f, int lane) {
+    const int t = lane & 3;
+    const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+#pragma unroll
+    for (int i = 0; i < kDimTiles; ++i) {
+      o[n][i][0] *= f0;
+      o[n][i][1] *= f1;
+      o[n][i][2] *= f0;
+      o[n][i][3] *= f1;
+    }
+  }
+  // image in memory: float j of lane at p[32 j + lane]
+  template <class F>
+  __device__ __forceinline__ void each(F f) {
+    int j = 0;
+#pragma unroll
+    for (int n = 0; n < NH; ++n) {
+      f(m[n], j++);
+      f(l[n], j++);
+    }
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int i = 0; i < kDimTiles; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(o[n][i][e], j++);
+  }
+};
+
+// out[b][head][dim] and lse of a finished state (l reduced, V's scale applied by the caller's vs)
+template <int DP, int NH>
+__device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, int b, int vh, float vs, int lane) {
+  constexpr int VB = DP / 8;
+  const int g = lane >> 2, t = lane & 3;
+  const int kvh = vh / p.row_tiles, r0 = (vh - kvh * p.row_tiles) * 8 * NH;
+  const int D = p.c.head_dim;
+#pragma unroll
+  for (int n = 0; n < NH; ++n) {
+    const int row = r0 + 8 * n + g;
+    if (p.lse && t == 0 && row < p.group)
+      p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + row] =
+          s.l[n] == 0.0f ? -INFINITY : kLn2 * (s.m[n] + lg2(s.l[n]));
+    s.scale_rows(n, __fdiv_rn(vs, s.l[n]), lane);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = r0 + 8 * n + 2 * t + e;
+      if (r >= p.group) continue;
+      uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D + g * VB;
+#pragma unroll
+      for (int c = 0; c < VB / 8; ++c) {
+        if (g * VB + 8 * c >= D) continue;
+        uint4 w;
+        w.x = f32x2_to_bf16x2(s.o[n][4 * c + 0][e], s.o[n][4 * c + 0][2 + e]);
+        w.y = f32x2_to_bf16x2(s.o[n][4 * c + 1][e], s.o[n][4 * c + 1][2 + e]);
+        w.z = f32x2_to_bf16x2(s.o[n][4 * c + 2][e], s.o[n][4 * c + 2][2 + e]);
+        w.w = f32x2_to_bf16x2(s.o[n][4 * c + 3][e], s.o[n][4 * c + 3][2 + e]);
+        *reinterpret_cast<uint4*>(dst + 8 * c) = w;
+      }
+    }
+  }
+}
+
+// Position of 16-byte piece `c` of row `row` in a stage: pieces are exchanged within a row so that
+// the eight threads of a shared-memory access phase (rows g, g + 1 and pieces t of K; rows 2t and
+// pieces g, g + 1 of V) fall on different banks for 128-byte rows.
+template <int DP>
+__device__ __forceinline__ int swizzled(int row, int c) {
+  if constexpr (DP == 64) {
+    return c ^ (((row >> 1) & 1) << 1);
+  } else {
+    return c ^ ((((row >> 1) & 3) << 1) ^ ((row & 1) << 2));
+  }
+}
+
+template <int DP>
+constexpr int kStageBytes = 2 * kAttnTile * DP + 2 * kAttnTile * 4;
+
+template <int FMT, int DP, int NH, bool TOKEN_SCALES>
+__global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attention(const Params p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t sh_sum[kWarps];
+  __shared__ int64_t sh_total, sh_base;
+  __shared__ int sh_req;
+  constexpr int DPC = DP / 16;               // 16-byte pieces of a padded row
+  constexpr int RPI = 32 / DPC;              // rows one warp-wide copy covers
+  constexpr int VB = DP / 8;
+  using St = State<DP, NH>;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nwarps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int phase = warp / p.heads_per_block;
+  const int vh = blockIdx.y * p.heads_per_block + warp % p.heads_per_block;
+  const bool active = vh < p.vheads;         // the last group of heads may be short
+  const int kvh = active ? vh / p.row_tiles : 0;
+  const int r0 = active ? (vh - kvh * p.row_tiles) * 8 * NH : 0;
+  const int D = p.c.head_dim;
+
+  allow_dependent_launch();
+  grid_dependency_wait();
+
+  // ---- total number of tiles, and this block's share of them
+  int64_t mine = 0;
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
+    mine += attn_range(clamped_len(p, b), p.window, p.sinks).tiles;
+  int64_t sum = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) sh_sum[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int64_t a = 0;
+    for (int w = 0; w < nwarps; ++w) a += sh_sum[w];
+    sh_total = a;
+  }
+  __syncthreads();
+  const int64_t total = sh_total;
+  const int workers = attn_workers(total, p.workers, kMinTiles);
+  const int w = blockIdx.x;
+  if (blockIdx.y == 0 && threadIdx.x == 0 && p.desc) p.desc[w] = make_int4(-1, 0, 0, 0);
+
+  // requests without a visible token: zeros, and an empty sum
+  for (int b = w; b < p.batch; b += p.workers) {
+    if (clamped_len(p, b) > 0) continue;
+    if (active && phase == 0) {
+      for (int r = r0; r < min(p.group, r0 + 8 * NH); ++r) {
+        uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D;
+        if (8 * lane < D) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0, 0, 0, 0);
+        if (p.lse && lane == 0) p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = -INFINITY;
+      }
+    }
+  }
+  if (w >= workers || total == 0) return;
+  const int64_t t_begin = attn_start(total, workers, w), t_end = attn_start(total, workers, w + 1);
+
+  // ---- the request that holds tile t_begin, and the tiles before it
+  if (threadIdx.x == 0) sh_req = p.batch;
+  {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
+      const int b = b0 + threadIdx.x;
+      const int64_t n = b < p.batch ? attn_range(clamped_len(p, b), p.window, p.sinks).tiles : 0;
+      int64_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      __syncthreads();                       // sh_sum of the round before has been read
+      if (lane == 31) sh_sum[warp] = incl;
+      __syncthreads();
+      int64_t before = base, all = base;
+      for (int k = 0; k < nwarps; ++k) {
+        if (k < warp) before += sh_sum[k];
+        all += sh_sum[k];
+      }
+      if (n > 0 && before + incl - n <= t_begin && t_begin < before + incl) {
+        sh_req = b;
+        sh_base = before + incl - n;
+      }
+      base = all;
+      if (all > t_begin) break;              // the same for every thread
+    }
+    __syncthreads();
+  }
+  int b = sh_req;
+  int64_t base = sh_base;
+
+  uint8_t* ring = smem + (size_t)warp * (kStages * kStageBytes<DP>);
+  const uint32_t ring_u = smem_u32(ring);
+  float vscale = 1.0f, kscale = 1.0f;
+  if constexpr (!TOKEN_SCALES) {
+    const int i = p.c.gran == 0 ? 0 : kvh;
+    kscale = __ldg(p.c.ks + i);
+    vscale = __ldg(p.c.vs + i);
+  }
+  const uint8_t* kbase = p.c.k + (int64_t)kvh * p.c.head_stride;
+  const uint8_t* vbase = p.c.v + (int64_t)kvh * p.c.head_stride;
+  const bool tile_in_page = p.c.page_size % kAttnTile == 0;
+
+  for (int64_t at = t_begin; at < t_end && b < p.batch; ++b) {
+    const int n = clamped_len(p, b);
+    const AttnRange range = attn_range(n, p.window, p.sinks);
+    if (range.tiles == 0) continue;
+    const int first = (int)(at - base);
+    const int last = (int)min((int64_t)range.tiles, t_end - base);   // one past this block's last tile
+    St s;
+    s.clear();
+
+    if (active) {
+      // ---- query rows as A fragments: f16 after a power of two that brings the row's largest
+      // element to 2^14 .. 2^15; the inverse power joins the score's factor
+      uint32_t qa[NH][DP / 64][8];
+      float qmul[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const int r = r0 + 8 * h + g;
+        const uint16_t* src = p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + min(r, p.group - 1)) * D;
+        uint32_t raw[DP / 64][8];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j) {
+          const int c = t + 4 * j;
+          uint4 x = make_uint4(0, 0, 0, 0), y = x;
+          if (r < p.group && 16 * c < D) {
+            x = __ldg(reinterpret_cast<const uint4*>(src + 16 * c));
+            y = __ldg(reinterpret_cast<const uint4*>(src + 16 * c + 8));
+          }
+          raw[j][0] = x.x, raw[j][1] = x.y, raw[j][2] = x.z, raw[j][3] = x.w;
+          raw[j][4] = y.x, raw[j][5] = y.y, raw[j][6] = y.z, raw[j][7] = y.w;
+          mx = absmax_v4(absmax_v4(mx, x), y);
+        }
+        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const uint32_t ex = __float_as_uint(packed_amax_to_f32(mx)) >> 23;   // biased exponent of the largest
+        const uint32_t up = ex == 255u ? 127u : min(268u - ex, 253u);
+        const float f = __uint_as_float(up << 23);
+        qmul[h] = __uint_as_float((254u - up) << 23) * p.scale2 * kscale;
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) qa[h][j][i] = pack_f16(bf16_lo(raw[j][i]) * f, bf16_hi(raw[j][i]) * f);
+      }
+
+      const int* row_table = p.table + (int64_t)b * p.max_pages;
+      // token of tile i's first row
+      auto tile_token = [&](int i) { return (i < range.head ? i : i + range.skip) * kAttnTile; };
+      auto visible = [&](int tok) {
+        return tok < n && (p.window == 0 || tok >= n - p.window || tok < p.sinks);
+      };
+      // page of this lane's token (lane % 16) of tile i, or -1 where nothing is to be read
+      auto page_of = [&](int i) {
+        if (i >= last) return -1;
+        const int tok = tile_token(i) + (tile_in_page ? 0 : (lane & 15));
+        return tok < n ? __ldg(row_table + div_u32((uint32_t)tok, p.c.page_div)) : -1;
+      };
+      auto issue = [&](int i, int stage, int page) {
+        if (i < last) {
+          const int tok0 = tile_token(i);
+          const int tok = tok0 + (lane & 15);
+          const bool ok = (uint32_t)page < (uint32_t)p.c.num_pages;
+          if (!ok && visible(tok)) raise_device_error(p.err, kErrBadPage);
+          const int off = tok - (int)(div_u32((uint32_t)tok, p.c.page_div) * (uint32_t)p.c.page_size);
+          const int64_t place = ok ? (int64_t)page * p.c.page_stride + (int64_t)off * p.c.token_stride : 0;
+          const uint32_t seen = __ballot_sync(0xFFFFFFFFu, ok && visible(tok));
+          const uint32_t dst = ring_u + stage * kStageBytes<DP>;
+          const int c = lane % DPC;
+#pragma unroll
+          for (int k = 0; k < kAttnTile / RPI; ++k) {
+            const int row = k * RPI + lane / DPC;
+            const int64_t from = __shfl_sync(0xFFFFFFFFu, place, row) + 16 * c;
+            const bool take = ((seen >> row) & 1u) && 16 * c < D;
+            const uint32_t to = dst + row * DP + 16 * swizzled<DP>(row, c);
+            cp_async16(to, kbase + (take ? from : 0), take);
+            cp_async16(to + kAttnTile * DP, vbase + (take ? from : 0), take);
+          }
+          if constexpr (TOKEN_SCALES) {
+            const bool take = (seen >> (lane & 15)) & 1u;
+            const int64_t slot = take ? (int64_t)page * p.c.page_size + off : 0;
+            const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
+                                                   : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
+            cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale, take);
+          }
+        }
+        cp_async_commit();
+      };
+
+      const int step = p.phases;
+      int i_load = first + phase;
+      int page = page_of(i_load);
+#pragma unroll
+      for (int k = 0; k < kStages - 1; ++k) {
+        const int next = page_of(i_load + step);
+        issue(i_load, k, page);
+        page = next;
+        i_load += step;
+      }
+      int stage = 0;
+      for (int i = first + phase; i < last; i += step) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();                        // the stage has landed for every lane; the one before is read out
+        {
+          const int next = page_of(i_load + step);
+          issue(i_load, stage == 0 ? kStages - 1 : stage - 1, page);
+          page = next;
+          i_load += step;
+        }
+        const uint8_t* ks = ring + stage * kStageBytes<DP>;
+        const uint8_t* vs = ks + kAttnTile * DP;
+        const float* sc = reinterpret_cast<const float*>(vs + kAttnTile * DP);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+
+        // ---- S = q K^T, 16 tokens
+        float sc4[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc4[j][e] = 0.0f;
+          const int row = 8 * j + g;
+#pragma unroll
+          for (int d = 0; d < DP / 64; ++d) {
+            const uint4 x = ld_shared_v4(ks + row * DP + 16 * swizzled<DP>(row, t + 4 * d));
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              mma_f16(sc4[j], qa[0][d][2 * m], NH == 2 ? qa[NH - 1][d][2 * m] : 0u, qa[0][d][2 * m + 1],
+                      NH == 2 ? qa[NH - 1][d][2 * m + 1] : 0u, fp8x2_to_f16x2<FMT>((uint16_t)(xw[m] & 0xFFFFu)),
+                      fp8x2_to_f16x2<FMT>((uint16_t)(xw[m] >> 16)));
+          }
+        }
+
+        // ---- softmax weights of tokens 8 j + 2 t + e, row tile h
+        const int tok0 = tile_token(i);
+        const bool whole = tok0 + kAttnTile <= n &&
+                           (p.window == 0 || tok0 >= n - p.window || tok0 + kAttnTile <= p.sinks);
+        float kf[2][2], vf[2][2], vl[2][2];
+        if constexpr (TOKEN_SCALES) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              kf[j][e] = sc[8 * j + 2 * t + e];
+              vf[j][e] = sc[16 + 8 * j + 2 * t + e];
+              vl[j][e] = lg2(fmaxf(vf[j][e], 0x1.0p-60f));
+            }
+        }
+        uint32_t pb[NH][2];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          float z[2][2];
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              z[j][e] = sc4[j][2 * h + e] * qmul[h];
+              if constexpr (TOKEN_SCALES) z[j][e] *= kf[j][e];
+              if (!whole && !visible(tok0 + 8 * j + 2 * t + e)) z[j][e] = -INFINITY;
+              // V's scale counts towards the running maximum, so a weight times its scale is at
+              // most 1 when it is rounded to f16
+              if constexpr (TOKEN_SCALES) top = fmaxf(top, z[j][e] + vl[j][e]);
+              else top = fmaxf(top, z[j][e]);
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          if (__any_sync(0xFFFFFFFFu, top > s.m[h])) {
+            const float m_new = fmaxf(s.m[h], top);
+            const float f = m_new == -INFINITY ? 1.0f : ex2(s.m[h] - m_new);
+            s.m[h] = m_new;
+            s.l[h] *= f;
+            s.scale_rows(h, f, lane);
+          }
+          const float mr = s.m[h] == -INFINITY ? 0.0f : s.m[h];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float a = ex2(z[j][0] - mr), c = ex2(z[j][1] - mr);
+            s.l[h] += a + c;
+            if constexpr (TOKEN_SCALES) a *= vf[j][0], c *= vf[j][1];
+            pb[h][j] = pack_f16(a, c);
+          }
+        }
+
+        // ---- O^T += V^T P^T
+        constexpr int VW = VB / 4;           // words of a row a thread reads
+        uint32_t v[4][VW];                   // rows 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = 2 * t + (k & 1) + 8 * (k >> 1);
+          if constexpr (DP == 64) {
+            const uint2 x = ld_shared_v2(vs + row * DP + 16 * swizzled<DP>(row, g >> 1) + 8 * (g & 1));
+            v[k][0] = x.x, v[k][1] = x.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < VB / 16; ++c) {
+              const uint4 x = ld_shared_v4(vs + row * DP + 16 * swizzled<DP>(row, g * (VB / 16) + c));
+              v[k][4 * c] = x.x, v[k][4 * c + 1] = x.y, v[k][4 * c + 2] = x.z, v[k][4 * c + 3] = x.w;
+            }
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < VW; ++m) {
+          // bytes of both tokens side by side: dims 4 m, 4 m + 1 and 4 m + 2, 4 m + 3
+          const uint32_t x0 = __byte_perm(v[0][m], v[1][m], 0x5140), x1 = __byte_perm(v[0][m], v[1][m], 0x7362);
+          const uint32_t y0 = __byte_perm(v[2][m], v[3][m], 0x5140), y1 = __byte_perm(v[2][m], v[3][m], 0x7362);
+          const uint32_t a0 = fp8x2_to_f16x2<FMT>((uint16_t)(x0 & 0xFFFFu)), a1 = fp8x2_to_f16x2<FMT>((uint16_t)(x0 >> 16));
+          const uint32_t a2 = fp8x2_to_f16x2<FMT>((uint16_t)(y0 & 0xFFFFu)), a3 = fp8x2_to_f16x2<FMT>((uint16_t)(y0 >> 16));
+          const uint32_t c0 = fp8x2_to_f16x2<FMT>((uint16_t)(x1 & 0xFFFFu)), c1 = fp8x2_to_f16x2<FMT>((uint16_t)(x1 >> 16));
+          const uint32_t c2 = fp8x2_to_f16x2<FMT>((uint16_t)(y1 & 0xFFFFu)), c3 = fp8x2_to_f16x2<FMT>((uint16_t)(y1 >> 16));
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            mma_f16(s.o[h][2 * m], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+            mma_f16(s.o[h][2 * m + 1], c0, c1, c2, c3, pb[h][0], pb[h][1]);
+          }
+        }
+      }
+      cp_async_wait<0>();
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        s.l[h] += __shfl_xor_sync(0xFFFFFFFFu, s.l[h], 1);
+        s.l[h] += __shfl_xor_sync(0xFFFFFFFFu, s.l[h], 2);
+      }
+      __syncwarp();                          // every lane has read the last stages
+    }
+
+    // ---- warps that shared a head's tiles: the first adds up the others' states
+    if (p.phases > 1) {
+      __syncthreads();
+      if (active && phase > 0) {
+        float* image = reinterpret_cast<float*>(ring);
+        s.each([&](float& x, int j) { image[32 * j + lane] = x; });
+      }
+      __syncthreads();
+      if (active && phase == 0) {
+        for (int k = 1; k < p.phases; ++k) {
+          const float* image = reinterpret_cast<const float*>(
+              smem + (size_t)(warp + k * p.heads_per_block) * (kStages * kStageBytes<DP>));
+          St u;
+          u.each([&](float& x, int j) { x = image[32 * j + lane]; });
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float m_new = fmaxf(s.m[h], u.m[h]);
+            const float f = ex2_diff(s.m[h], m_new), fu = ex2_diff(u.m[h], m_new);
+            s.m[h] = m_new;
+            s.l[h] = s.l[h] * f + u.l[h] * fu;
+            s.scale_rows(h, f, lane);
+            u.scale_rows(h, fu, lane);
+#pragma unroll
+            for (int i = 0; i < St::kDimTiles; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s.o[h][i][e] += u.o[h][i][e];
+          }
+        }
+      }
+      __syncthreads();                       // the images are read before the ring is filled again
+    }
+
+    if (active && phase == 0) {
+      if (first == 0 && last == range.tiles) {
+        write_rows<DP, NH>(p, s, b, vh, vscale, lane);
+      } else {
+        // a request's part that begins where this block's range begins goes to place 0, else to 1
+        const int place = at == t_begin ? 0 : 1;
+        float* image = p.part + ((int64_t)(2 * w + place) * p.vheads + vh) * (32 * St::kFloats);
+        s.each([&](float& x, int j) { image[32 * j + lane] = x; });
+      }
+    }
+    if (first == 0 && last < range.tiles && blockIdx.y == 0 && threadIdx.x == 0)
+      p.desc[w] = make_int4(b, at == t_begin ? 0 : 1, w,
+                            min(workers - 1, attn_owner(total, workers, base + range.tiles - 1)));
+    base += range.tiles;
+    at = base < t_end ? base : t_end;
+  }
+}
+
+// Second launch: adds up the parts of each shared request.  A block takes (request, vhead) pairs;
+// its warps take every kJoinWarps-th part and are joined in shared memory in their order.
+template <int DP, int NH, bool TOKEN_SCALES>
+__global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p) {
+  using St = State<DP, NH>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int4 list[kJoinThreads];
+  __shared__ int count;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  allow_dependent_launch();
+  grid_dependency_wait();
+  for (int w0 = 0; w0 < p.workers; w0 += kJoinThreads) {
+    __syncthreads();
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    const int w = w0 + threadIdx.x;
+    const int4 d = w < p.workers ? p.desc[w] : make_int4(-1, 0, 0, 0);
+    if (d.x >= 0) list[atomicAdd(&count, 1)] = d;      // any order: each entry is joined by itself
+    __syncthreads();
+    // the list's order differs from block to block, so entries are taken by their worker
+    for (int k = 0; k < count; ++k) {
+      const int4 e = list[k];
+      for (int vh = 0; vh < p.vheads; ++vh) {
+        if ((int)((e.z * (int64_t)p.vheads + vh) % gridDim.x) != (int)blockIdx.x) continue;
+        St s;
+        s.clear();
+        for (int x = e.z + warp; x <= e.w; x += kJoinWarps) {
+          const int place = x == e.z ? e.y : 0;
+          const float* image = p.part + ((int64_t)(2 * x + place) * p.vheads + vh) * (32 * St::kFloats);
+          St u;
+          u.each([&](float& y, int j) { y = image[32 * j + lane]; });
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const float m_new = fmaxf(s.m[h], u.m[h]);
+            const float f = ex2_diff(s.m[h], m_new), fu = ex2_diff(u.m[h], m_new);
+            s.m[h] = m_new;
+            s.l[h] = s.l[h] * f + u.l[h] * fu;
+            s.scale_rows(h, f, lane);
+            u.scale_rows(h, fu, lane);
+#pragma unroll
+            for (int i = 0; i < St::kDimTiles; ++i)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) s.o[h][i][q] += u.o[h][i][q];
+          }
+        }
+        float* image = reinterpret_cast<float*>(smem);
+        if (warp > 0) s.each([&](float& y, int j) { image[(warp - 1) * 32 * St::kFloats + 32 * j + lane] = y; });
+        __syncthreads();
+        if (warp == 0) {
+          for (int k2 = 1; k2 < kJoinWarps; ++k2) {
+            St u;
+            u.each([&](float& y, int j) { y = image[(k2 - 1) * 32 * St::kFloats + 32 * j + lane]; });
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              const float m_new = fmaxf(s.m[h], u.m[h]);
+              const float f = ex2_diff(s.m[h], m_new), fu = ex2_diff(u.m[h], m_new);
+              s.m[h] = m_new;
+              s.l[h] = s.l[h] * f + u.l[h] * fu;
+              s.scale_rows(h, f, lane);
+              u.scale_rows(h, fu, lane);
+#pragma unroll
+              for (int i = 0; i < St::kDimTiles; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) s.o[h][i][q] += u.o[h][i][q];
+            }
+          }
+          float vs = 1.0f;
+          if constexpr (!TOKEN_SCALES) vs = __ldg(p.c.vs + (p.c.gran == 0 ? 0 : vh / p.row_tiles));
+          write_rows<DP, NH>(p, s, e.x, vh, vs, lane);
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+struct Shape {
+  int dp, nh;              // padded head_dim, query-row tiles of 8 a warp holds
+  int row_tiles, vheads;   // query-row groups per key-value head, pairs in all
+  int heads_per_block, phases, groups, workers;
+  int64_t image;           // floats of one partial result
+};
+
+// head_dim is padded to 64, 128 or 256.  Groups above 8 query heads use both row halves of the
+// first product (two tiles a warp) where the registers suffice.
+inline Shape shape_of(int heads, int group, int head_dim) {
+  Shape s;
+  s.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+  s.nh = group > 8 && s.dp <= 128 ? 2 : 1;
+  s.row_tiles = (group + 8 * s.nh - 1) / (8 * s.nh);
+  s.vheads = heads * s.row_tiles;
+  s.groups = (s.vheads + kWarps - 1) / kWarps;
+  s.heads_per_block = (s.vheads + s.groups - 1) / s.groups;
+  s.phases = kWarps / s.heads_per_block;
+  const int per_sm = s.dp * s.nh <= 128 ? 2 : 1;
+  s.workers = std::max(1, device_sm_count() * per_sm / s.groups);
+  s.image = 32 * s.nh * (s.dp / 4 + 2);
+  return s;
+}
+
+template <int FMT, int DP, int NH, bool TOKEN_SCALES>
+cudaError_t launch(const Params& p, const Shape& s, bool join, cudaStream_t st) {
+  const int warps = s.heads_per_block * s.phases;
+  const size_t smem = (size_t)warps * kStages * kStageBytes<DP>;
+  auto* kernel = k_attention<FMT, DP, NH, TOKEN_SCALES>;
+  cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(s.workers, s.groups), dim3(32 * warps), smem, st, p);
+  if (e != cudaSuccess || !join) return e;
+  auto* joiner = k_attention_join<DP, NH, TOKEN_SCALES>;
+  const size_t jsmem = (size_t)(kJoinWarps - 1) * s.image * 4;
+  e = ensure_dynamic_smem((const void*)joiner, jsmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(joiner, dim3(std::max(1, device_sm_count())), dim3(kJoinThreads), jsmem, st, p);
+}
+
+template <int FMT, bool TOKEN_SCALES>
+cudaError_t launch_dims(const Params& p, const Shape& s, bool join, cudaStream_t st) {
+  if (s.dp == 64)
+    return s.nh == 1 ? launch<FMT, 64, 1, TOKEN_SCALES>(p, s, join, st) : launch<FMT, 64, 2, TOKEN_SCALES>(p, s, join, st);
+  if (s.dp == 128)
+    return s.nh == 1 ? launch<FMT, 128, 1, TOKEN_SCALES>(p, s, join, st) : launch<FMT, 128, 2, TOKEN_SCALES>(p, s, join, st);
+  return launch<FMT, 256, 1, TOKEN_SCALES>(p, s, join, st);
+}
+
+// No request is shared when a single worker takes all tiles there can be.
+inline bool may_share(int64_t batch, int64_t max_tokens) {
+  return batch * ((max_tokens + kAttnTile - 1) / kAttnTile) > kMinTiles;
+}
+
+}  // namespace attn
+
+// Walks every worker's share with the kernel's own functions: each tile of each request is held
+// once, a worker holds parts of at most two shared requests (the first and the last of its range),
+// and the workers named by a shared request's descriptor are those that hold its tiles.
+int check_attention_split(const int* lens, int64_t batch, int window, int sinks, int most) {
+  if (batch < 0 || most < 1 || window < 0 || sinks < 0 || (batch > 0 && !lens)) return -1;
+  int64_t total = 0;
+  for (int64_t b = 0; b < batch; ++b) {
+    const AttnRange r = attn_range(lens[b], window, sinks);
+    if (r.tiles < 0 || r.head > r.tiles || r.skip < 0) return 1;
+    // the tiles in order hold every visible token and end with the last one's
+    for (int tok = 0; tok < lens[b]; ++tok) {
+      if (window > 0 && tok < lens[b] - window && tok >= sinks) continue;
+      const int tile = tok / kAttnTile;
+      const int i = tile < r.head ? tile : tile - r.skip;
+      if (i < 0 || i >= r.tiles || (i < r.head ? i : i + r.skip) != tile) return 2;
+    }
+    total += r.tiles;
+  }
+  if (total == 0) return 0;
+  const int workers = attn_workers(total, most, attn::kMinTiles);
+  if (workers < 1 || workers > most) return 3;
+  int64_t expect = 0;
+  for (int w = 0; w < workers; ++w) {
+    if (attn_start(total, workers, w) != expect) return 4;
+    expect = attn_start(total, workers, w + 1);
+    if (expect <= attn_start(total, workers, w)) return 5;       // every worker has work
+    for (int64_t x = attn_start(total, workers, w); x < expect; ++x)
+      if (attn_owner(total, workers, x) != w) return 6;
+  }
+  if (expect != total) return 7;
+  int64_t base = 0;
+  for (int64_t b = 0; b < batch; ++b) {
+    const int n = attn_range(lens[b], window, sinks).tiles;
+    if (n == 0) continue;
+    const int first = attn_owner(total, workers, base), last = attn_owner(total, workers, base + n - 1);
+    for (int w = first; w <= last; ++w) {
+      const int64_t from = std::max(base, attn_start(total, workers, w));
+      const int64_t to = std::min(base + n, attn_start(total, workers, w + 1));
+      if (from >= to) return 8;                                   // a named worker without a part
+      // place 0 is the part at the beginning of a range, place 1 the one at its end
+      const bool at_begin = from == attn_start(total, workers, w);
+      if (first != last && !at_begin && to != attn_start(total, workers, w + 1)) return 9;
+      if (w > first && !at_begin) return 10;
+    }
+    base += n;
+  }
+  return 0;
+}
+
+size_t attention_workspace_bytes(int64_t batch, int64_t max_tokens, int heads, int group, int head_dim) {
+  if (!attn::may_share(batch, max_tokens)) return 0;
+  const attn::Shape s = attn::shape_of(heads, group, head_dim);
+  return (size_t)s.workers * 16 + 256 + (size_t)2 * s.workers * s.vheads * s.image * 4;
+}
+
+cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q, int64_t q_stride, int group,
+                                   const int* table, int64_t batch, int64_t max_pages, const int* lens, float scale,
+                                   int window, int sinks, uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                   cudaStream_t st) {
+  const attn::Shape s = attn::shape_of(c.heads, group, c.head_dim);
+  attn::Params p;
+  p.c = c;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.table = table;
+  p.lens = lens;
+  p.batch = (int)batch;
+  p.max_pages = (int)max_pages;
+  p.group = group;
+  p.window = window;
+  p.sinks = sinks;
+  p.scale2 = scale * attn::kLog2e;
+  p.out = out;
+  p.out_stride = out_stride;
+  p.lse = lse;
+  p.vheads = s.vheads;
+  p.row_tiles = s.row_tiles;
+  p.heads_per_block = s.heads_per_block;
+  p.phases = s.phases;
+  p.workers = s.workers;
+  const bool join = attn::may_share(batch, max_pages * c.page_size);
+  p.desc = join ? static_cast<int4*>(ws) : nullptr;
+  p.part = join ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)s.workers * 16 + 255) / 256 * 256) : nullptr;
+  p.err = device_error_word();
+  const bool token_scales = c.gran >= 2;
+  if (fmt == kE4M3)
+    return token_scales ? attn::launch_dims<kE4M3, true>(p, s, join, st) : attn::launch_dims<kE4M3, false>(p, s, join, st);
+  return token_scales ? attn::launch_dims<kE5M2, true>(p, s, join, st) : attn::launch_dims<kE5M2, false>(p, s, join, st);
+}
+
+}  // namespace fp8q

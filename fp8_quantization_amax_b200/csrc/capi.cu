@@ -4,8 +4,11 @@
 
 #include <cstdint>
 
+#include <cmath>
+
 #include "fp8q.h"
 #include "internal.h"
+#include "kv_pages.cuh"
 
 namespace fp8q {
 cudaError_t launch_selftest_wait(cudaStream_t st);
@@ -30,6 +33,41 @@ int64_t checked_elems(int64_t a, int64_t b) {
   if (a == 0 || b == 0) return 0;
   if (a > kMaxElems / b) return -1;
   return a * b;
+}
+
+constexpr int64_t kMaxTableTokens = (int64_t(1) << 31) - 65;   // token numbers and slots fit an int
+
+// A paged cache from the caller's description; FP8Q_OK and *out, or the reason why not.
+fp8q_status paged_cache(const fp8q_kv_pages* c, fp8q::KvPages* out) {
+  if (!c || !valid_fmt(c->f) || c->g < FP8Q_KV_PER_TENSOR || c->g > FP8Q_KV_PER_TOKEN) return FP8Q_ERR_INVALID_ARGUMENT;
+  if (c->num_pages < 0 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1) return FP8Q_ERR_INVALID_ARGUMENT;
+  if (c->head_dim % 16 != 0 || c->page_stride % 16 != 0 || c->token_stride % 16 != 0 || c->head_stride % 16 != 0)
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (c->head_dim > 256 || c->heads > 65536 || c->page_size > kMaxTableTokens ||
+      (c->num_pages > 0 && c->page_size > kMaxTableTokens / c->num_pages))
+    return FP8Q_ERR_UNSUPPORTED;
+  // places of different tokens, heads or pages do not overlap
+  if ((c->heads > 1 && c->head_stride < c->head_dim) || (c->page_size > 1 && c->token_stride < c->head_dim) ||
+      (c->num_pages > 1 && c->page_stride < c->head_dim))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (!c->k_scales || !c->v_scales || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (c->num_pages > 0 && (!c->k_codes || !c->v_codes || !aligned(c->k_codes, 16) || !aligned(c->v_codes, 16)))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  out->k = c->k_codes;
+  out->v = c->v_codes;
+  out->ks = c->k_scales;
+  out->vs = c->v_scales;
+  out->page_stride = c->page_stride;
+  out->token_stride = c->token_stride;
+  out->head_stride = c->head_stride;
+  out->num_pages = (int)c->num_pages;
+  out->page_size = (int)c->page_size;
+  out->heads = (int)c->heads;
+  out->head_dim = (int)c->head_dim;
+  out->gran = c->g;
+  out->page_div = fp8q::make_fastdiv((uint32_t)c->page_size);
+  return FP8Q_OK;
 }
 
 fp8q_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FP8Q_OK : FP8Q_ERR_CUDA; }
@@ -439,6 +477,179 @@ fp8q_status fp8_gemm_mx(const uint8_t* A, const uint8_t* sA, fp8q_format fa, con
     return FP8Q_ERR_INVALID_ARGUMENT;
   return from_cuda(fp8q::launch_gemm_mx(A, sA, fa, B, sB, fb, M, N, K, static_cast<uint16_t*>(C),
                                         (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ paged KV cache
+
+size_t fp8q_pages_workspace_bytes(int64_t batch, int64_t max_tokens) {
+  if (batch < 0 || max_tokens < 0) return 0;
+  return fp8q::pages_workspace_bytes(batch, max_tokens);
+}
+
+fp8q_status fp8_kv_pages_update(int32_t* block_table, int64_t batch, int64_t max_pages, int64_t page_size,
+                                const int32_t* lens, const int32_t* added, int32_t* lens_out, int32_t* free_pages,
+                                int64_t num_pages, const int32_t* free_count, int32_t* free_count_out,
+                                int64_t max_tokens, int64_t* slots, int32_t* positions, int32_t* offsets,
+                                int32_t* served, void* ws, size_t ws_bytes, fp8q_stream_t stream) {
+  if (batch < 0 || max_pages < 0 || page_size < 1 || num_pages < 0 || max_tokens < 0) return FP8Q_ERR_INVALID_ARGUMENT;
+  if (page_size > kMaxTableTokens || batch > kMaxTableTokens || max_tokens > kMaxTableTokens ||
+      (max_pages > 0 && page_size > kMaxTableTokens / max_pages) ||
+      (batch > 0 && max_pages > kMaxTableTokens / batch) || (num_pages > 0 && page_size > kMaxTableTokens / num_pages))
+    return FP8Q_ERR_UNSUPPORTED;
+  if (!free_count || !free_count_out || !offsets || !aligned(free_count, 4) || !aligned(free_count_out, 4) ||
+      !aligned(offsets, 4) || (num_pages > 0 && (!free_pages || !aligned(free_pages, 4))))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (batch > 0 && (!lens || !added || !lens_out || !served || !aligned(lens, 4) || !aligned(added, 4) ||
+                    !aligned(lens_out, 4) || !aligned(served, 4) ||
+                    (max_pages > 0 && (!block_table || !aligned(block_table, 4)))))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (max_tokens > 0 && (!slots || !positions || !aligned(slots, 8) || !aligned(positions, 4)))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  const size_t need = fp8q::pages_workspace_bytes(batch, max_tokens);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) return FP8Q_ERR_WORKSPACE;
+  fp8q::PagesUpdate u;
+  u.table = block_table;
+  u.batch = batch;
+  u.max_pages = max_pages;
+  u.page_size = page_size;
+  u.lens = lens;
+  u.added = added;
+  u.lens_out = lens_out;
+  u.free_pages = free_pages;
+  u.num_pages = num_pages;
+  u.free_count = free_count;
+  u.free_count_out = free_count_out;
+  u.max_tokens = max_tokens;
+  u.slots = slots;
+  u.positions = positions;
+  u.offsets = offsets;
+  u.served = served;
+  u.ws = ws;
+  return from_cuda(fp8q::launch_pages_update(u, (cudaStream_t)stream));
+}
+
+fp8q_status fp8q_rope_turns(int64_t rot_dim, double base, fp8q_rope_kind kind, double factor, double original_len,
+                            double low, double high, uint64_t* turns, float* gain) {
+  if (rot_dim < 0 || rot_dim > 256 || rot_dim % 8 != 0 || !(base > 0.0) || !std::isfinite(base) ||
+      kind < FP8Q_ROPE_PLAIN || kind > FP8Q_ROPE_RAMP || !gain || (rot_dim > 0 && !turns))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (kind != FP8Q_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return FP8Q_ERR_INVALID_ARGUMENT;
+  if (kind >= FP8Q_ROPE_SMOOTH &&
+      (!(original_len > 0.0) || !std::isfinite(original_len) || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (kind == FP8Q_ROPE_RAMP && !(base > 1.0)) return FP8Q_ERR_INVALID_ARGUMENT;
+  const double two_pi = 6.283185307179586476925;
+  for (int64_t i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * (double)i / (double)rot_dim);    // radians per position
+    const double periods = original_len * f / two_pi;                 // turns over the original length
+    if (kind == FP8Q_ROPE_LINEAR) {
+      f /= factor;
+    } else if (kind == FP8Q_ROPE_SMOOTH) {
+      const double keep = std::fmin(1.0, std::fmax(0.0, (periods - low) / (high - low)));
+      f = (1.0 - keep) * f / factor + keep * f;
+    } else if (kind == FP8Q_ROPE_RAMP) {
+      // pair numbers whose turns over the original length are `high` and `low`, to whole pairs
+      const double half = 0.5 * (double)rot_dim / std::log(base);
+      const double from = std::fmax(0.0, std::floor(half * std::log(original_len / (high * two_pi))));
+      double to = std::fmin((double)(rot_dim - 1), std::ceil(half * std::log(original_len / (low * two_pi))));
+      if (to <= from) to = from + 0.001;
+      const double stretch = std::fmin(1.0, std::fmax(0.0, ((double)i - from) / (to - from)));
+      f = (1.0 - stretch) * f + stretch * f / factor;
+    }
+    const double turn = f / two_pi;
+    // the fraction of a turn in units of 2^-64 (positions are whole numbers: whole turns vanish)
+    turns[i] = (uint64_t)std::nearbyint(std::ldexp(turn - std::floor(turn), 64));
+  }
+  *gain = kind == FP8Q_ROPE_RAMP ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return FP8Q_OK;
+}
+
+fp8q_status fp8_kv_append(const fp8q_kv_pages* cache, const void* q, int64_t q_stride, int64_t q_heads, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens, const int64_t* slots,
+                          const int32_t* positions, const uint64_t* turns, int64_t rot_dim, int interleaved, float gain,
+                          const void* q_weight, const void* k_weight, float eps, void* q_out, int64_t q_out_stride,
+                          fp8q_stream_t stream) {
+  fp8q::KvPages c;
+  const fp8q_status st = paged_cache(cache, &c);
+  if (st != FP8Q_OK) return st;
+  if (tokens < 0 || q_heads < 0 || rot_dim < 0 || rot_dim % 8 != 0 || rot_dim > cache->head_dim || !(eps >= 0.0f))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (cache->g == FP8Q_KV_PER_HEAD_TOK128) return FP8Q_ERR_UNSUPPORTED;   // a block's amax needs all its tokens
+  if (tokens > kMaxTableTokens || q_heads > 65536) return FP8Q_ERR_UNSUPPORTED;
+  if (tokens == 0) return FP8Q_OK;
+  const int64_t kv_row = cache->heads * cache->head_dim, q_row = q_heads * cache->head_dim;
+  if (!k || !v || !slots || !aligned(k, 8) || !aligned(v, 8) || !aligned(slots, 8) || k_stride % 4 != 0 ||
+      v_stride % 4 != 0 || (tokens > 1 && (k_stride < kv_row || v_stride < kv_row)))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (q_heads > 0 && (!q || !q_out || !aligned(q, 8) || !aligned(q_out, 8) || q_stride % 4 != 0 ||
+                      q_out_stride % 4 != 0 || (tokens > 1 && (q_stride < q_row || q_out_stride < q_row))))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (rot_dim > 0 && (!positions || !turns || !aligned(positions, 4) || !aligned(turns, 8)))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if ((q_weight && !aligned(q_weight, 8)) || (k_weight && !aligned(k_weight, 8))) return FP8Q_ERR_INVALID_ARGUMENT;
+  fp8q::KvAppend a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_heads = (int)q_heads;
+  a.tokens = tokens;
+  a.slots = slots;
+  a.positions = positions;
+  a.turns = reinterpret_cast<const unsigned long long*>(turns);
+  a.rot = (int)rot_dim;
+  a.interleaved = interleaved != 0;
+  a.gain = gain;
+  a.q_weight = static_cast<const uint16_t*>(q_weight);
+  a.k_weight = static_cast<const uint16_t*>(k_weight);
+  a.eps = eps;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_out_stride = q_out_stride;
+  return from_cuda(fp8q::launch_kv_append(c, cache->f, a, (cudaStream_t)stream));
+}
+
+size_t fp8q_attention_workspace_bytes(int64_t batch, int64_t max_tokens, int64_t q_heads, int64_t kv_heads,
+                                      int64_t head_dim) {
+  if (batch <= 0 || max_tokens <= 0 || q_heads < 1 || kv_heads < 1 || kv_heads > 65536 || q_heads > 65536 ||
+      q_heads % kv_heads != 0 || head_dim < 1 || head_dim > 256 || batch > kMaxTableTokens ||
+      max_tokens > kMaxTableTokens)
+    return 0;
+  return fp8q::attention_workspace_bytes(batch, max_tokens, (int)kv_heads, (int)(q_heads / kv_heads), (int)head_dim);
+}
+
+int fp8q_check_attention_split(const int32_t* lens, int64_t batch, int64_t window, int64_t sinks, int workers) {
+  if (window > kMaxTableTokens || sinks > kMaxTableTokens) return -1;
+  return fp8q::check_attention_split(lens, batch, (int)window, (int)sinks, workers);
+}
+
+fp8q_status fp8_attention_paged(const fp8q_kv_pages* cache, const void* q, int64_t q_stride, int64_t q_heads,
+                                const int32_t* block_table, int64_t batch, int64_t max_pages, const int32_t* lens,
+                                float scale, int64_t window, int64_t sinks, void* out, int64_t out_stride, float* lse,
+                                void* ws, size_t ws_bytes, fp8q_stream_t stream) {
+  fp8q::KvPages c;
+  const fp8q_status st = paged_cache(cache, &c);
+  if (st != FP8Q_OK) return st;
+  if (batch < 0 || max_pages < 0 || q_heads < 1 || q_heads % cache->heads != 0 || window < 0 || sinks < 0 ||
+      !(scale > 0.0f) || !std::isfinite(scale))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  if (q_heads > 65536 || batch > kMaxTableTokens || (max_pages > 0 && cache->page_size > kMaxTableTokens / max_pages))
+    return FP8Q_ERR_UNSUPPORTED;
+  if (batch == 0) return FP8Q_OK;
+  const int64_t row = q_heads * cache->head_dim;
+  if (!q || !out || !lens || !aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) || q_stride % 8 != 0 ||
+      out_stride % 8 != 0 || (batch > 1 && (q_stride < row || out_stride < row)) || (lse && !aligned(lse, 4)) ||
+      (max_pages > 0 && (!block_table || !aligned(block_table, 4))))
+    return FP8Q_ERR_INVALID_ARGUMENT;
+  const size_t need = fp8q_attention_workspace_bytes(batch, max_pages * cache->page_size, q_heads, cache->heads,
+                                                     cache->head_dim);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 16))) return FP8Q_ERR_WORKSPACE;
+  const int64_t limit = kMaxTableTokens;
+  return from_cuda(fp8q::launch_attention_paged(
+      c, cache->f, static_cast<const uint16_t*>(q), q_stride, (int)(q_heads / cache->heads), block_table, batch,
+      max_pages, lens, scale, (int)(window < limit ? window : limit), (int)(sinks < limit ? sinks : limit),
+      static_cast<uint16_t*>(out), out_stride, lse, ws, (cudaStream_t)stream));
 }
 
 }  // extern "C"

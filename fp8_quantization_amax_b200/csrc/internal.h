@@ -150,4 +150,53 @@ size_t linear_fused_workspace_bytes(int64_t M, int64_t K);
 cudaError_t launch_linear_fused(const uint16_t* X, const uint8_t* B, const float* sB, int gB, int64_t M, int64_t N,
                                 int64_t K, uint16_t* C, void* act_ws, cudaStream_t st);
 
+// paged KV cache (kv_pages.cuh)
+struct KvPages;
+
+// new tokens: norm and rotation of q and k, k and v quantized into their slots
+struct KvAppend {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;   // elements from token to token
+  int q_heads;
+  int64_t tokens;
+  const int64_t* slots;
+  const int* positions;
+  const unsigned long long* turns;
+  int rot, interleaved;
+  float gain;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  uint16_t* q_out;
+  int64_t q_out_stride;
+};
+cudaError_t launch_kv_append(const KvPages& c, int fmt, const KvAppend& a, cudaStream_t st);
+
+// block tables, slots and positions from the requests' lengths; ws: pages_workspace_bytes, scratch
+struct PagesUpdate {
+  int* table;
+  int64_t batch, max_pages, page_size;
+  const int *lens, *added;
+  int* lens_out;
+  int* free_pages;
+  int64_t num_pages;
+  const int* free_count;
+  int* free_count_out;
+  int64_t max_tokens;
+  int64_t* slots;
+  int *positions, *offsets, *served;
+  void* ws;
+};
+size_t pages_workspace_bytes(int64_t batch, int64_t max_tokens);
+cudaError_t launch_pages_update(const PagesUpdate& u, cudaStream_t st);
+
+// host only: consistency of the attention's division of work (fp8q_check_attention_split)
+int check_attention_split(const int* lens, int64_t batch, int window, int sinks, int workers);
+
+// attention of one token per request over its pages; ws: attention_workspace_bytes, scratch
+size_t attention_workspace_bytes(int64_t batch, int64_t max_tokens, int heads, int group, int head_dim);
+cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q, int64_t q_stride, int group,
+                                   const int* table, int64_t batch, int64_t max_pages, const int* lens, float scale,
+                                   int window, int sinks, uint16_t* out, int64_t out_stride, float* lse, void* ws,
+                                   cudaStream_t st);
+
 }  // namespace fp8q

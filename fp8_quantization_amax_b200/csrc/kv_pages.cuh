@@ -1,0 +1,85 @@
+// The paged FP8 KV cache as the kernels see it, and the small pieces the paged operators share.
+#pragma once
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace fp8q {
+
+// Codes of page p, token t of the page, head h, element d of K and V sit at byte
+// p * page_stride + t * token_stride + h * head_stride + d.  The slot of that token is
+// p * page_size + t.
+struct KvPages {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int64_t page_stride, token_stride, head_stride;
+  int num_pages, page_size, heads, head_dim;
+  int gran;            // fp8q_kv_granularity
+  FastDiv page_div;    // division by page_size
+};
+
+__device__ __forceinline__ uint32_t div_u32(uint32_t n, const FastDiv& f) {
+  return (uint32_t)(((uint64_t)__umulhi(n, f.m) + n) >> f.s);
+}
+
+// 4-, 16-byte asynchronous copy to shared memory; with !valid nothing is read and zeros are written
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------- division of the attention's work
+//
+// A request of n tokens is read in tiles of 16 tokens.  With a window only the tiles that hold a
+// visible token count: those of the first `sinks` tokens and those from token n - window on.  All
+// requests' tiles, laid end to end, are divided evenly over the workers.
+constexpr int kAttnTile = 16;
+
+struct AttnRange {
+  int tiles;      // tiles to read
+  int head;       // the first `head` of them begin at token 0 ...
+  int skip;       // ... and the others this many tiles further on
+};
+
+__host__ __device__ __forceinline__ AttnRange attn_range(int n, int window, int sinks) {
+  AttnRange r;
+  r.tiles = (n + kAttnTile - 1) / kAttnTile;
+  r.head = r.tiles;
+  r.skip = 0;
+  if (window > 0 && n > window) {
+    const int first = (n - window) / kAttnTile;                    // tile of the window's first token
+    const int front = ((sinks < n ? sinks : n) + kAttnTile - 1) / kAttnTile;
+    if (first > front) {
+      r.skip = first - front;
+      r.head = front;
+      r.tiles -= r.skip;
+    }
+  }
+  return r;
+}
+
+// workers that take part: at least `least` tiles each, so short work is not split without need
+__host__ __device__ __forceinline__ int attn_workers(int64_t tiles, int most, int least) {
+  const int64_t w = (tiles + least - 1) / least;
+  return (int)(w < 1 ? 1 : (w < most ? w : most));
+}
+
+// first tile of worker w; the worker that holds tile x
+__host__ __device__ __forceinline__ int64_t attn_start(int64_t tiles, int workers, int w) {
+  return tiles * w / workers;
+}
+__host__ __device__ __forceinline__ int attn_owner(int64_t tiles, int workers, int64_t x) {
+  return (int)(((x + 1) * workers - 1) / tiles);
+}
+
+}  // namespace fp8q

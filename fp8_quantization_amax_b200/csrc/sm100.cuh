@@ -20,6 +20,8 @@ namespace fp8q {
 constexpr uint32_t kErrWaitTimeout = 1u;
 // a workspace counter held a value no call leaves behind (workspace not zero-filled)
 constexpr uint32_t kErrWorkspaceDirty = 2u;
+// a page index, slot or page count outside the paged KV cache; what it named was not touched
+constexpr uint32_t kErrBadPage = 4u;
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // 2 s
 

@@ -93,7 +93,8 @@ typedef enum {
 typedef enum {
     FP8Q_KV_PER_TENSOR = 0,      /* one scale for K, one for V ([M] section 二)           */
     FP8Q_KV_PER_HEAD = 1,        /* one scale per head, separately for K and V ([P] 1)    */
-    FP8Q_KV_PER_HEAD_TOK128 = 2  /* one per head and 128-token block ([P] section 3)       */
+    FP8Q_KV_PER_HEAD_TOK128 = 2, /* one per head and 128-token block ([P] section 3)       */
+    FP8Q_KV_PER_TOKEN = 3        /* one per head and token: paged caches only ([W] 激活动态量化) */
 } fp8q_kv_granularity;
 
 /* Human-readable name of a status code (static storage; never NULL). */
@@ -107,7 +108,8 @@ FP8Q_API int fp8q_version(void);
  * 0: no error.  Bit 0: a bounded wait inside a kernel (a pipeline barrier that never completed)
  * gave up after its time limit, so that kernel's outputs are incomplete.  Bit 1: a GEMM
  * workspace was not zero-filled (see fp8_gemm_blockscaled), so some output tiles were not
- * written.  0xFFFFFFFF: the device could not be queried (e.g. an earlier fault).
+ * written.  Bit 2: a paged KV-cache call met a page, slot, length or free-page count outside the
+ * cache; memory outside it was neither read nor written.  0xFFFFFFFF: the device could not be queried (e.g. an earlier fault).
  */
 FP8Q_API uint32_t fp8q_device_status(void);
 
@@ -500,6 +502,150 @@ FP8Q_API fp8q_status fp8_linear_dynamic(const void *X, int64_t M, int64_t N, int
 FP8Q_API fp8q_status fp8_gemm_mx(const uint8_t *A, const uint8_t *sA, fp8q_format fa, const uint8_t *B,
                                  const uint8_t *sB, fp8q_format fb, int64_t M, int64_t N, int64_t K, void *C,
                                  fp8q_stream_t stream);
+
+/* ---------------------------------------------------------------- paged KV cache */
+
+/*
+ * A KV cache kept as FP8 codes in pages of page_size tokens, shared by many requests: a row of a
+ * block table names a request's pages in order.  The SLOT of a token is page * page_size + its
+ * place in the page, 0 <= slot < S = num_pages * page_size.  The code of element d of head h of a
+ * slot's token sits at byte page * page_stride + place * token_stride + h * head_stride + d, in K
+ * and in V, so [page][token][head][dim] and [page][head][token][dim] caches are both described
+ * (codes written by fp8_kv_quantize, [tokens][heads][head_dim], are pages as they stand).
+ *   f        one format for K and V
+ *   g        FP8Q_KV_PER_TENSOR       scales [1]
+ *            FP8Q_KV_PER_HEAD         scales [heads]
+ *            FP8Q_KV_PER_HEAD_TOK128  scales [ceil(S/128)][heads], of 128 consecutive slots
+ *            FP8Q_KV_PER_TOKEN        scales [heads][S] (the 1x128 layout of [W] 激活动态量化 where
+ *                                     head_dim is 128: a head's token scales are contiguous)
+ * Requirements: head_dim a multiple of 16, at most 256; strides multiples of 16 bytes; code
+ * pointers 16-byte aligned; num_pages * page_size below 2^31 - 64.
+ */
+typedef struct {
+  uint8_t *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+  int64_t num_pages, page_size, heads, head_dim;
+  int64_t page_stride, token_stride, head_stride;
+  fp8q_format f;
+  fp8q_kv_granularity g;
+} fp8q_kv_pages;
+
+/*
+ * The page bookkeeping of one serving step, on the device: block tables, slots and positions
+ * from the requests' lengths.
+ *   block_table     int32 [batch][max_pages] (read, written): the pages of each request in order;
+ *                   entries past ceil(len / page_size) are neither read nor written
+ *   lens            int32 [batch]: tokens each request holds
+ *   added           int32 [batch]: tokens each appends now; negative: the request ends
+ *   lens_out        int32 [batch] (written; may be lens): the lengths afterwards
+ *   free_pages      int32 [num_pages] (read, written): the first *free_count entries are the free
+ *                   pages, taken from the end
+ *   free_count, free_count_out   int32 [1] (read; written, may be the same)
+ *   slots           int64 [max_tokens], positions int32 [max_tokens] (written): of the added tokens,
+ *                   request after request
+ *   offsets         int32 [batch + 1] (written): where each request's tokens begin in them
+ *   served          int32 [batch] (written): 1 where the tokens were placed
+ *   ws              fp8q_pages_workspace_bytes(batch, max_tokens) bytes, scratch (NULL when 0)
+ * Requests that end give their pages back first, request after request, and their length becomes
+ * 0.  The others then take pages in order.  A request is served when its table row and max_tokens
+ * hold its tokens and it needs no page, or its pages and those wanted by the requests before it
+ * are there; else its length stays and its tokens get slot -1.  Entries of slots past the last
+ * token are -1, of positions 0.  Results do not depend on timing.  Lengths outside 0 ..
+ * max_pages * page_size, counts outside 0 .. num_pages and pages given back beyond num_pages are
+ * clipped and raise device error bit 2.  A step that failed can be repeated with the same inputs
+ * (lens_out and free_count_out apart): the same pages are taken again.
+ */
+FP8Q_API size_t fp8q_pages_workspace_bytes(int64_t batch, int64_t max_tokens);
+FP8Q_API fp8q_status fp8_kv_pages_update(int32_t *block_table, int64_t batch, int64_t max_pages, int64_t page_size,
+                                         const int32_t *lens, const int32_t *added, int32_t *lens_out,
+                                         int32_t *free_pages, int64_t num_pages, const int32_t *free_count,
+                                         int32_t *free_count_out, int64_t max_tokens, int64_t *slots,
+                                         int32_t *positions, int32_t *offsets, int32_t *served, void *ws,
+                                         size_t ws_bytes, fp8q_stream_t stream);
+
+/*
+ * Rotary frequencies as the append reads them (host only, host pointers): turns[i], i <
+ * rot_dim / 2, is the fraction of a turn that pair i advances per position, in units of 2^-64.
+ * A position times it, modulo 2^64, is the angle exactly to the last bits at any position.
+ * Radians per position are f_i = base^(-2 i / rot_dim), then by kind (factor >= 1 is the ratio of
+ * the context's length to original_len, the length trained on):
+ *   FP8Q_ROPE_PLAIN   f_i
+ *   FP8Q_ROPE_LINEAR  f_i / factor: positions interpolated
+ *   FP8Q_ROPE_SMOOTH  with n_i = original_len f_i / 2 pi turns over the original length: f_i where
+ *                     n_i >= high, f_i / factor where n_i <= low, in between the two mixed by
+ *                     (n_i - low) / (high - low)
+ *   FP8Q_ROPE_RAMP    mixed linearly in the pair number between the pairs of `high` and of `low`
+ *                     turns (B. Peng et al., "YaRN", arXiv 2309.00071, section 3.2, to whole
+ *                     pairs), and *gain = 0.1 ln(factor) + 1; the other kinds give *gain = 1
+ * rot_dim a multiple of 8, at most 256.  Unused arguments are ignored.
+ */
+typedef enum { FP8Q_ROPE_PLAIN = 0, FP8Q_ROPE_LINEAR = 1, FP8Q_ROPE_SMOOTH = 2, FP8Q_ROPE_RAMP = 3 } fp8q_rope_kind;
+FP8Q_API fp8q_status fp8q_rope_turns(int64_t rot_dim, double base, fp8q_rope_kind kind, double factor,
+                                     double original_len, double low, double high, uint64_t *turns, float *gain);
+
+/*
+ * New tokens into the cache, in one pass over the projection's output: per-head RMS norm and
+ * rotation of q and k, k and v quantized into their slots, q back as bf16.
+ *   q, k, v       bf16 [tokens][heads][head_dim] each, heads of a token contiguous, tokens
+ *                 *_stride elements apart (parts of one [tokens][q_heads + 2 heads][head_dim] output
+ *                 qualify); q may be NULL with q_heads = 0
+ *   slots         int64 [tokens]: where each token goes; negative: not at all (padding).  A slot
+ *                 beyond the cache is left out and raises device error bit 2.  Slots of one call
+ *                 must differ
+ *   q_weight, k_weight   bf16 [head_dim] or NULL: y = x / sqrt(mean(x^2) + eps) * w over each head
+ *   positions     int32 [tokens], turns uint64 [rot_dim / 2] (device; fp8q_rope_turns): the first
+ *                 rot_dim elements of each head of q and k are rotated, pairs (i, i + rot_dim / 2)
+ *                 or, interleaved, (2 i, 2 i + 1); cos and sin are multiplied by gain.  Both NULL
+ *                 with rot_dim = 0
+ *   q_out         bf16 [tokens][q_heads][head_dim] (written; may be q with the same stride)
+ * All of it is computed in fp32 from the bf16 inputs, q rounded to bf16 and k, v to codes once:
+ * code = FP8_RNE_SAT(y / s), the quotient in fp32 (v, and k without norm and rotation, to the bit as
+ * fp8_quantize; s = 0 gives signed zeros).  FP8Q_KV_PER_TENSOR and FP8Q_KV_PER_HEAD read the cache's
+ * scales (calibrated, or followed by fp8_kv_quantize_delayed); FP8Q_KV_PER_TOKEN writes
+ * s = amax / FMAX of each row; FP8Q_KV_PER_HEAD_TOK128 needs whole blocks: FP8Q_ERR_UNSUPPORTED.
+ * Requirements: rot_dim % 8 == 0; q, k, v, q_out and weights 8-byte aligned, strides multiples of 4.
+ */
+FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_pages *cache, const void *q, int64_t q_stride, int64_t q_heads,
+                                   const void *k, int64_t k_stride, const void *v, int64_t v_stride, int64_t tokens,
+                                   const int64_t *slots, const int32_t *positions, const uint64_t *turns,
+                                   int64_t rot_dim, int interleaved, float gain, const void *q_weight,
+                                   const void *k_weight, float eps, void *q_out, int64_t q_out_stride,
+                                   fp8q_stream_t stream);
+
+/*
+ * Attention of one new token per request over its pages:
+ *   z_j = scale * s_k(j) * sum_d q[d] decode(K_j[d]),  out = sum_j softmax(z)_j s_v(j) decode(V_j)
+ * for each query head over the request's visible tokens; q_heads / heads query heads share a
+ * key-value head.  Sums and softmax in fp32, the softmax weights rounded to f16 for the product.
+ *   q             bf16 [batch][q_heads][head_dim], requests q_stride elements apart
+ *   block_table   int32 [batch][max_pages], lens int32 [batch]: as fp8_kv_pages_update leaves them;
+ *                 lens counts the new token (append it first)
+ *   window        0: all tokens are visible; else the last `window` tokens and the first `sinks`.
+ *                 Pages without a visible token are not read, nor is their table entry used
+ *   out           bf16 [batch][q_heads][head_dim], requests out_stride elements apart (written)
+ *   lse           NULL, or fp32 [batch][q_heads] (written): log of the softmax's denominator, ln sum
+ *                 exp(z), with which parts of a longer context can be joined
+ *   ws            fp8q_attention_workspace_bytes(batch, max_pages * page_size, ...) bytes, 16-byte
+ *                 aligned, scratch without initialisation (NULL when 0); calls that may run at the
+ *                 same time need separate ones
+ * A request of length 0 gives zeros and lse = -inf.  Codes and scales of tokens that are not
+ * visible, whatever they hold, do not reach the result.  A visible token's page outside the cache is
+ * read as zeros and raises device error bit 2; lengths are clipped to 0 .. max_pages * page_size.
+ * Results do not depend on timing (parts of a shared request are added in a fixed order).
+ * fp8q_check_attention_split (host only, host pointer): walks the division of the requests' tiles
+ * over `workers` blocks with the kernel's own functions; 0 when every visible token is read exactly
+ * once and every part is found by the join, a positive code for the first violation, -1 for a bad
+ * argument.
+ * Requirements: q_heads % heads == 0; q and out 16-byte aligned, strides multiples of 8; scale > 0.
+ */
+FP8Q_API size_t fp8q_attention_workspace_bytes(int64_t batch, int64_t max_tokens, int64_t q_heads, int64_t kv_heads,
+                                               int64_t head_dim);
+FP8Q_API int fp8q_check_attention_split(const int32_t *lens, int64_t batch, int64_t window, int64_t sinks, int workers);
+FP8Q_API fp8q_status fp8_attention_paged(const fp8q_kv_pages *cache, const void *q, int64_t q_stride, int64_t q_heads,
+                                         const int32_t *block_table, int64_t batch, int64_t max_pages,
+                                         const int32_t *lens, float scale, int64_t window, int64_t sinks, void *out,
+                                         int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                                         fp8q_stream_t stream);
 
 #ifdef __cplusplus
 }
