@@ -43,12 +43,13 @@
 namespace fp8q {
 namespace attn {
 
-constexpr int kWarps = 8;
+constexpr int kMaxWarps = 16;
+constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
 constexpr int kMinTiles = 4;
-constexpr int kStages = 3;
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
+constexpr int kJoinBatch = 4;                 // parts whose loads are in flight together
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -112,7 +113,6 @@ __device__ __forceinline__ int clamped_len(const Params& p, int b) {
 template <int DP, int NH>
 struct State {
   static constexpr int kDimTiles = DP / 16;
-  static constexpr int kFloats = NH * (4 * kDimTiles + 2);
   float m[NH], l[NH], o[NH][kDimTiles][4];
 
   __device__ __forceinline__ void clear() {
@@ -138,21 +138,41 @@ struct State {
       o[n][i][3] *= f1;
     }
   }
-  // image in memory: float j of lane at p[32 j + lane]
-  template <class F>
-  __device__ __forceinline__ void each(F f) {
-    int j = 0;
+  // The state in memory, so that a warp's accesses are contiguous: m and l of tile n at floats
+  // 64 n + lane and 64 n + 32 + lane, then o[n][i] as the float4 32 (n kDimTiles + i) + lane.
+  static constexpr int kImage = 32 * NH * (2 + 4 * kDimTiles);
+  __device__ __forceinline__ void store(float* image, int lane) const {
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-      f(m[n], j++);
-      f(l[n], j++);
-    }
-#pragma unroll
-    for (int n = 0; n < NH; ++n)
+      image[64 * n + lane] = m[n];
+      image[64 * n + 32 + lane] = l[n];
 #pragma unroll
       for (int i = 0; i < kDimTiles; ++i)
+        reinterpret_cast<float4*>(image + 64 * NH)[32 * (n * kDimTiles + i) + lane] =
+            make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+    }
+  }
+  // add a state of other tokens
+  __device__ __forceinline__ void add(const float* image, int lane) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f(o[n][i][e], j++);
+    for (int n = 0; n < NH; ++n) {
+      const float um = image[64 * n + lane], ul = image[64 * n + 32 + lane];
+      const float m_new = fmaxf(m[n], um);
+      const float f = ex2_diff(m[n], m_new), fu = ex2_diff(um, m_new);
+      m[n] = m_new;
+      l[n] = l[n] * f + ul * fu;
+      scale_rows(n, f, lane);
+      const int t = lane & 3;
+      const float u0 = __shfl_sync(0xFFFFFFFFu, fu, 8 * t), u1 = __shfl_sync(0xFFFFFFFFu, fu, 8 * t + 4);
+#pragma unroll
+      for (int i = 0; i < kDimTiles; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(image + 64 * NH)[32 * (n * kDimTiles + i) + lane];
+        o[n][i][0] += x.x * u0;
+        o[n][i][1] += x.y * u1;
+        o[n][i][2] += x.z * u0;
+        o[n][i][3] += x.w * u1;
+      }
+    }
   }
 };
 
@@ -203,20 +223,46 @@ __device__ __forceinline__ int swizzled(int row, int c) {
 
 template <int DP>
 constexpr int kStageBytes = 2 * kAttnTile * DP + 2 * kAttnTile * 4;
+template <int DP>
+constexpr int kStagesOf = DP == 64 ? 5 : 3;
+
+// One block per SM.  Up to 128 registers a thread 16 warps share an SM; two row tiles of 128 dims or
+// one of 256 need more, and 8 warps.
+constexpr int warps_of(int dp, int nh) { return dp * nh <= 128 ? 16 : 8; }
+
+// Sum over the threads up to and including this one, and over the block
+__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh, int64_t* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += up;
+  }
+  __syncthreads();                           // sh of the call before has been read
+  if (lane == 31) sh[warp] = v;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int k = 0; k < (int)(blockDim.x >> 5); ++k) {
+    if (k < warp) before += sh[k];
+    total += sh[k];
+  }
+  *all = total;
+  return v + before;
+}
 
 template <int FMT, int DP, int NH, bool TOKEN_SCALES>
-__global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attention(const Params p) {
+__global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sh_sum[kWarps];
-  __shared__ int64_t sh_total, sh_base;
+  __shared__ int64_t sh_sum[kMaxWarps];
+  __shared__ int64_t sh_base;
   __shared__ int sh_req;
   constexpr int DPC = DP / 16;               // 16-byte pieces of a padded row
   constexpr int RPI = 32 / DPC;              // rows one warp-wide copy covers
   constexpr int VB = DP / 8;
+  constexpr int kStages = kStagesOf<DP>;
   using St = State<DP, NH>;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nwarps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int phase = warp / p.heads_per_block;
   const int vh = blockIdx.y * p.heads_per_block + warp % p.heads_per_block;
@@ -225,73 +271,61 @@ __global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attenti
   const int r0 = active ? (vh - kvh * p.row_tiles) * 8 * NH : 0;
   const int D = p.c.head_dim;
 
+  if (threadIdx.x == 0) sh_req = p.batch;
   allow_dependent_launch();
   grid_dependency_wait();
 
-  // ---- total number of tiles, and this block's share of them
-  int64_t mine = 0;
-  for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
-    mine += attn_range(clamped_len(p, b), p.window, p.sinks).tiles;
-  int64_t sum = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) sh_sum[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int64_t a = 0;
-    for (int w = 0; w < nwarps; ++w) a += sh_sum[w];
-    sh_total = a;
+  // ---- total number of tiles; this block's share of them, and the request it begins in.  With at
+  // most one request a thread one sum over the block gives both.
+  const bool single = p.batch <= (int)blockDim.x;
+  int64_t tiles = 0, total = 0, upto = 0;
+  bool empty = false;
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+    const int n = attn_range(clamped_len(p, b), p.window, p.sinks).tiles;
+    tiles += n;
+    empty |= n == 0;
   }
-  __syncthreads();
-  const int64_t total = sh_total;
+  upto = block_sum(tiles, sh_sum, &total);
   const int workers = attn_workers(total, p.workers, kMinTiles);
   const int w = blockIdx.x;
   if (blockIdx.y == 0 && threadIdx.x == 0 && p.desc) p.desc[w] = make_int4(-1, 0, 0, 0);
 
   // requests without a visible token: zeros, and an empty sum
-  for (int b = w; b < p.batch; b += p.workers) {
-    if (clamped_len(p, b) > 0) continue;
-    if (active && phase == 0) {
-      for (int r = r0; r < min(p.group, r0 + 8 * NH); ++r) {
-        uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D;
-        if (8 * lane < D) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0, 0, 0, 0);
-        if (p.lse && lane == 0) p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = -INFINITY;
+  if (__syncthreads_or(empty)) {
+    for (int b = w; b < p.batch; b += p.workers) {
+      if (clamped_len(p, b) > 0) continue;
+      if (active && phase == 0) {
+        for (int r = r0; r < min(p.group, r0 + 8 * NH); ++r) {
+          uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D;
+          if (8 * lane < D) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0, 0, 0, 0);
+          if (p.lse && lane == 0) p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = -INFINITY;
+        }
       }
     }
   }
   if (w >= workers || total == 0) return;
   const int64_t t_begin = attn_start(total, workers, w), t_end = attn_start(total, workers, w + 1);
-
-  // ---- the request that holds tile t_begin, and the tiles before it
-  if (threadIdx.x == 0) sh_req = p.batch;
-  {
-    int64_t base = 0;
+  if (single) {
+    if (tiles > 0 && upto - tiles <= t_begin && t_begin < upto) {
+      sh_req = threadIdx.x;
+      sh_base = upto - tiles;
+    }
+  } else {
+    int64_t before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
       const int b = b0 + threadIdx.x;
       const int64_t n = b < p.batch ? attn_range(clamped_len(p, b), p.window, p.sinks).tiles : 0;
-      int64_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += up;
-      }
-      __syncthreads();                       // sh_sum of the round before has been read
-      if (lane == 31) sh_sum[warp] = incl;
-      __syncthreads();
-      int64_t before = base, all = base;
-      for (int k = 0; k < nwarps; ++k) {
-        if (k < warp) before += sh_sum[k];
-        all += sh_sum[k];
-      }
-      if (n > 0 && before + incl - n <= t_begin && t_begin < before + incl) {
+      int64_t all;
+      const int64_t incl = before + block_sum(n, sh_sum, &all);
+      if (n > 0 && incl - n <= t_begin && t_begin < incl) {
         sh_req = b;
-        sh_base = before + incl - n;
+        sh_base = incl - n;
       }
-      base = all;
-      if (all > t_begin) break;              // the same for every thread
+      before += all;
+      if (before > t_begin) break;           // the same for every thread
     }
-    __syncthreads();
   }
+  __syncthreads();
   int b = sh_req;
   int64_t base = sh_base;
 
@@ -317,40 +351,6 @@ __global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attenti
     s.clear();
 
     if (active) {
-      // ---- query rows as A fragments: f16 after a power of two that brings the row's largest
-      // element to 2^14 .. 2^15; the inverse power joins the score's factor
-      uint32_t qa[NH][DP / 64][8];
-      float qmul[NH];
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const int r = r0 + 8 * h + g;
-        const uint16_t* src = p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + min(r, p.group - 1)) * D;
-        uint32_t raw[DP / 64][8];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int j = 0; j < DP / 64; ++j) {
-          const int c = t + 4 * j;
-          uint4 x = make_uint4(0, 0, 0, 0), y = x;
-          if (r < p.group && 16 * c < D) {
-            x = __ldg(reinterpret_cast<const uint4*>(src + 16 * c));
-            y = __ldg(reinterpret_cast<const uint4*>(src + 16 * c + 8));
-          }
-          raw[j][0] = x.x, raw[j][1] = x.y, raw[j][2] = x.z, raw[j][3] = x.w;
-          raw[j][4] = y.x, raw[j][5] = y.y, raw[j][6] = y.z, raw[j][7] = y.w;
-          mx = absmax_v4(absmax_v4(mx, x), y);
-        }
-        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const uint32_t ex = __float_as_uint(packed_amax_to_f32(mx)) >> 23;   // biased exponent of the largest
-        const uint32_t up = ex == 255u ? 127u : min(268u - ex, 253u);
-        const float f = __uint_as_float(up << 23);
-        qmul[h] = __uint_as_float((254u - up) << 23) * p.scale2 * kscale;
-#pragma unroll
-        for (int j = 0; j < DP / 64; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) qa[h][j][i] = pack_f16(bf16_lo(raw[j][i]) * f, bf16_hi(raw[j][i]) * f);
-      }
-
       const int* row_table = p.table + (int64_t)b * p.max_pages;
       // token of tile i's first row
       auto tile_token = [&](int i) { return (i < range.head ? i : i + range.skip) * kAttnTile; };
@@ -404,6 +404,40 @@ __global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attenti
         page = next;
         i_load += step;
       }
+      // ---- query rows as A fragments: f16 after a power of two that brings the row's largest
+      // element to 2^14 .. 2^15; the inverse power joins the score's factor
+      uint32_t qa[NH][DP / 64][8];
+      float qmul[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        const int r = r0 + 8 * h + g;
+        const uint16_t* src = p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + min(r, p.group - 1)) * D;
+        uint32_t raw[DP / 64][8];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j) {
+          const int c = t + 4 * j;
+          uint4 x = make_uint4(0, 0, 0, 0), y = x;
+          if (r < p.group && 16 * c < D) {
+            x = __ldg(reinterpret_cast<const uint4*>(src + 16 * c));
+            y = __ldg(reinterpret_cast<const uint4*>(src + 16 * c + 8));
+          }
+          raw[j][0] = x.x, raw[j][1] = x.y, raw[j][2] = x.z, raw[j][3] = x.w;
+          raw[j][4] = y.x, raw[j][5] = y.y, raw[j][6] = y.z, raw[j][7] = y.w;
+          mx = absmax_v4(absmax_v4(mx, x), y);
+        }
+        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        const uint32_t ex = __float_as_uint(packed_amax_to_f32(mx)) >> 23;   // biased exponent of the largest
+        const uint32_t up = ex == 255u ? 127u : min(268u - ex, 253u);
+        const float f = __uint_as_float(up << 23);
+        qmul[h] = __uint_as_float((254u - up) << 23) * p.scale2 * kscale;
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) qa[h][j][i] = pack_f16(bf16_lo(raw[j][i]) * f, bf16_hi(raw[j][i]) * f);
+      }
+
       int stage = 0;
       for (int i = first + phase; i < last; i += step) {
         cp_async_wait<kStages - 2>();
@@ -534,32 +568,12 @@ __global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attenti
     // ---- warps that shared a head's tiles: the first adds up the others' states
     if (p.phases > 1) {
       __syncthreads();
-      if (active && phase > 0) {
-        float* image = reinterpret_cast<float*>(ring);
-        s.each([&](float& x, int j) { image[32 * j + lane] = x; });
-      }
+      if (active && phase > 0) s.store(reinterpret_cast<float*>(ring), lane);
       __syncthreads();
-      if (active && phase == 0) {
-        for (int k = 1; k < p.phases; ++k) {
-          const float* image = reinterpret_cast<const float*>(
-              smem + (size_t)(warp + k * p.heads_per_block) * (kStages * kStageBytes<DP>));
-          St u;
-          u.each([&](float& x, int j) { x = image[32 * j + lane]; });
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const float m_new = fmaxf(s.m[h], u.m[h]);
-            const float f = ex2_diff(s.m[h], m_new), fu = ex2_diff(u.m[h], m_new);
-            s.m[h] = m_new;
-            s.l[h] = s.l[h] * f + u.l[h] * fu;
-            s.scale_rows(h, f, lane);
-            u.scale_rows(h, fu, lane);
-#pragma unroll
-            for (int i = 0; i < St::kDimTiles; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s.o[h][i][e] += u.o[h][i][e];
-          }
-        }
-      }
+      if (active && phase == 0)
+        for (int k = 1; k < p.phases; ++k)
+          s.add(reinterpret_cast<const float*>(smem + (size_t)(warp + k * p.heads_per_block) * (kStages * kStageBytes<DP>)),
+                lane);
       __syncthreads();                       // the images are read before the ring is filled again
     }
 
@@ -569,8 +583,7 @@ __global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attenti
       } else {
         // a request's part that begins where this block's range begins goes to place 0, else to 1
         const int place = at == t_begin ? 0 : 1;
-        float* image = p.part + ((int64_t)(2 * w + place) * p.vheads + vh) * (32 * St::kFloats);
-        s.each([&](float& x, int j) { image[32 * j + lane] = x; });
+        s.store(p.part + ((int64_t)(2 * w + place) * p.vheads + vh) * St::kImage, lane);
       }
     }
     if (first == 0 && last < range.tiles && blockIdx.y == 0 && threadIdx.x == 0)
@@ -581,77 +594,134 @@ __global__ void __launch_bounds__(32 * kWarps, DP * NH <= 128 ? 2 : 1) k_attenti
   }
 }
 
-// Second launch: adds up the parts of each shared request.  A block takes (request, vhead) pairs;
-// its warps take every kJoinWarps-th part and are joined in shared memory in their order.
+// Second launch: adds up the parts of each shared request.  A unit is a quarter of a part of 128
+// dims: two dim tiles of a row tile of one (request, vhead).  Where units are few, several warps
+// share one (each takes every wpu-th part) and are added in shared memory in their order.
 template <int DP, int NH, bool TOKEN_SCALES>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p) {
   using St = State<DP, NH>;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int4 list[kJoinThreads];
-  __shared__ int count;
+  constexpr int kPairs = St::kDimTiles / 2;
+  constexpr int kUnits = NH * kPairs;
+  constexpr int VB = DP / 8;
+  __shared__ int4 list[kMaxWorkers];
+  __shared__ int sh_count[kJoinWarps];
+  __shared__ float sh[kJoinWarps][12][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
   allow_dependent_launch();
   grid_dependency_wait();
+
+  // ---- the shared requests, in the workers' order
+  int count = 0;
   for (int w0 = 0; w0 < p.workers; w0 += kJoinThreads) {
-    __syncthreads();
-    if (threadIdx.x == 0) count = 0;
-    __syncthreads();
     const int w = w0 + threadIdx.x;
     const int4 d = w < p.workers ? p.desc[w] : make_int4(-1, 0, 0, 0);
-    if (d.x >= 0) list[atomicAdd(&count, 1)] = d;      // any order: each entry is joined by itself
+    const uint32_t has = __ballot_sync(0xFFFFFFFFu, d.x >= 0);
     __syncthreads();
-    // the list's order differs from block to block, so entries are taken by their worker
-    for (int k = 0; k < count; ++k) {
-      const int4 e = list[k];
-      for (int vh = 0; vh < p.vheads; ++vh) {
-        if ((int)((e.z * (int64_t)p.vheads + vh) % gridDim.x) != (int)blockIdx.x) continue;
-        St s;
-        s.clear();
-        for (int x = e.z + warp; x <= e.w; x += kJoinWarps) {
-          const int place = x == e.z ? e.y : 0;
-          const float* image = p.part + ((int64_t)(2 * x + place) * p.vheads + vh) * (32 * St::kFloats);
-          St u;
-          u.each([&](float& y, int j) { y = image[32 * j + lane]; });
+    if (lane == 0) sh_count[warp] = __popc(has);
+    __syncthreads();
+    int at = count + __popc(has & ((1u << lane) - 1u));
+    for (int k = 0; k < kJoinWarps; ++k) {
+      if (k < warp) at += sh_count[k];
+      count += sh_count[k];
+    }
+    if (d.x >= 0) list[at] = d;
+  }
+  __syncthreads();
+  const int64_t units = (int64_t)count * p.vheads * kUnits;
+  int wpu = 1;                               // warps a unit
+  while (wpu < kJoinWarps && units * (2 * wpu) <= (int64_t)gridDim.x * kJoinWarps) wpu *= 2;
+  const int per_block = kJoinWarps / wpu, mine = warp % wpu;
+  for (int64_t u0 = (int64_t)blockIdx.x * per_block; u0 < units; u0 += (int64_t)gridDim.x * per_block) {
+    const int64_t u = u0 + warp / wpu;
+    const bool live = u < units;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f, o[8];
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const float m_new = fmaxf(s.m[h], u.m[h]);
-            const float f = ex2_diff(s.m[h], m_new), fu = ex2_diff(u.m[h], m_new);
-            s.m[h] = m_new;
-            s.l[h] = s.l[h] * f + u.l[h] * fu;
-            s.scale_rows(h, f, lane);
-            u.scale_rows(h, fu, lane);
+    for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+    int4 e = make_int4(0, 0, 0, -1);
+    int vh = 0, n = 0, pair = 0;
+    if (live) {
+      const int part = (int)(u % kUnits);
+      const int64_t v = u / kUnits;
+      vh = (int)(v % p.vheads);
+      e = list[v / p.vheads];
+      n = part / kPairs;
+      pair = part % kPairs;
+      // rows 2t and 2t + 1 have their maximum and sum in lanes 8t and 8t + 4 of the image
+      for (int x0 = e.z + mine; x0 <= e.w; x0 += wpu * kJoinBatch) {
+        float um[kJoinBatch][2], ul[kJoinBatch][2];
+        float4 uo[kJoinBatch][2];
 #pragma unroll
-            for (int i = 0; i < St::kDimTiles; ++i)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) s.o[h][i][q] += u.o[h][i][q];
+        for (int k = 0; k < kJoinBatch; ++k) {
+          const int x = x0 + k * wpu;
+          um[k][0] = um[k][1] = -INFINITY;
+          ul[k][0] = ul[k][1] = 0.0f;
+          uo[k][0] = uo[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (x <= e.w) {
+            const float* image = p.part + ((int64_t)(2 * x + (x == e.z ? e.y : 0)) * p.vheads + vh) * St::kImage;
+            um[k][0] = image[64 * n + 8 * t];
+            um[k][1] = image[64 * n + 8 * t + 4];
+            ul[k][0] = image[64 * n + 32 + 8 * t];
+            ul[k][1] = image[64 * n + 32 + 8 * t + 4];
+            const float4* q = reinterpret_cast<const float4*>(image + 64 * NH) + 32 * (n * St::kDimTiles + 2 * pair) + lane;
+            uo[k][0] = q[0];
+            uo[k][1] = q[32];
           }
         }
-        float* image = reinterpret_cast<float*>(smem);
-        if (warp > 0) s.each([&](float& y, int j) { image[(warp - 1) * 32 * St::kFloats + 32 * j + lane] = y; });
-        __syncthreads();
-        if (warp == 0) {
-          for (int k2 = 1; k2 < kJoinWarps; ++k2) {
-            St u;
-            u.each([&](float& y, int j) { y = image[(k2 - 1) * 32 * St::kFloats + 32 * j + lane]; });
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-              const float m_new = fmaxf(s.m[h], u.m[h]);
-              const float f = ex2_diff(s.m[h], m_new), fu = ex2_diff(u.m[h], m_new);
-              s.m[h] = m_new;
-              s.l[h] = s.l[h] * f + u.l[h] * fu;
-              s.scale_rows(h, f, lane);
-              u.scale_rows(h, fu, lane);
+        for (int k = 0; k < kJoinBatch; ++k) {
+          const float a0 = fmaxf(m0, um[k][0]), a1 = fmaxf(m1, um[k][1]);
+          const float f0 = ex2_diff(m0, a0), f1 = ex2_diff(m1, a1);
+          const float h0 = ex2_diff(um[k][0], a0), h1 = ex2_diff(um[k][1], a1);
+          m0 = a0;
+          m1 = a1;
+          l0 = l0 * f0 + ul[k][0] * h0;
+          l1 = l1 * f1 + ul[k][1] * h1;
+          const float x[8] = {uo[k][0].x, uo[k][0].y, uo[k][0].z, uo[k][0].w, uo[k][1].x, uo[k][1].y, uo[k][1].z, uo[k][1].w};
 #pragma unroll
-              for (int i = 0; i < St::kDimTiles; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) s.o[h][i][q] += u.o[h][i][q];
-            }
-          }
-          float vs = 1.0f;
-          if constexpr (!TOKEN_SCALES) vs = __ldg(p.c.vs + (p.c.gran == 0 ? 0 : vh / p.row_tiles));
-          write_rows<DP, NH>(p, s, e.x, vh, vs, lane);
+          for (int j = 0; j < 8; ++j) o[j] = (j & 1) ? o[j] * f1 + x[j] * h1 : o[j] * f0 + x[j] * h0;
         }
-        __syncthreads();
+      }
+    }
+    if (wpu > 1) {
+      __syncthreads();                       // sh of the unit before has been read
+      sh[warp][0][lane] = m0;
+      sh[warp][1][lane] = m1;
+      sh[warp][2][lane] = l0;
+      sh[warp][3][lane] = l1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sh[warp][4 + j][lane] = o[j];
+      __syncthreads();
+      if (mine == 0) {
+        for (int k = warp + 1; k < warp + wpu; ++k) {
+          const float b0 = sh[k][0][lane], b1 = sh[k][1][lane];
+          const float a0 = fmaxf(m0, b0), a1 = fmaxf(m1, b1);
+          const float f0 = ex2_diff(m0, a0), f1 = ex2_diff(m1, a1), h0 = ex2_diff(b0, a0), h1 = ex2_diff(b1, a1);
+          m0 = a0;
+          m1 = a1;
+          l0 = l0 * f0 + sh[k][2][lane] * h0;
+          l1 = l1 * f1 + sh[k][3][lane] * h1;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = (j & 1) ? o[j] * f1 + sh[k][4 + j][lane] * h1 : o[j] * f0 + sh[k][4 + j][lane] * h0;
+        }
+      }
+    }
+    if (live && mine == 0) {
+      float vs = 1.0f;
+      if constexpr (!TOKEN_SCALES) vs = __ldg(p.c.vs + (p.c.gran == 0 ? 0 : vh / p.row_tiles));
+      const int kvh = vh / p.row_tiles, row = (vh - kvh * p.row_tiles) * 8 * NH + 8 * n + 2 * t;
+      const int dim = g * VB + 4 * pair;     // o holds dims dim .. dim + 3 of rows row, row + 1
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (row + r >= p.group) continue;
+        const float l = r ? l1 : l0, m = r ? m1 : m0, f = __fdiv_rn(vs, l);
+        const int64_t head = kvh * p.group + row + r;
+        if (p.lse && pair == 0 && g == 0)
+          p.lse[(int64_t)e.x * (p.c.heads * p.group) + head] = l == 0.0f ? -INFINITY : kLn2 * (m + lg2(l));
+        if (dim < p.c.head_dim)
+          *reinterpret_cast<uint2*>(p.out + (int64_t)e.x * p.out_stride + head * p.c.head_dim + dim) =
+              make_uint2(f32x2_to_bf16x2(o[r] * f, o[2 + r] * f), f32x2_to_bf16x2(o[4 + r] * f, o[6 + r] * f));
       }
     }
   }
@@ -674,11 +744,11 @@ inline Shape shape_of(int heads, int group, int head_dim) {
   s.nh = group > 8 && s.dp <= 128 ? 2 : 1;
   s.row_tiles = (group + 8 * s.nh - 1) / (8 * s.nh);
   s.vheads = heads * s.row_tiles;
-  s.groups = (s.vheads + kWarps - 1) / kWarps;
+  const int warps = warps_of(s.dp, s.nh);
+  s.groups = (s.vheads + warps - 1) / warps;
   s.heads_per_block = (s.vheads + s.groups - 1) / s.groups;
-  s.phases = kWarps / s.heads_per_block;
-  const int per_sm = s.dp * s.nh <= 128 ? 2 : 1;
-  s.workers = std::max(1, device_sm_count() * per_sm / s.groups);
+  s.phases = warps / s.heads_per_block;
+  s.workers = std::min(kMaxWorkers, std::max(1, device_sm_count() / s.groups));
   s.image = 32 * s.nh * (s.dp / 4 + 2);
   return s;
 }
@@ -686,17 +756,14 @@ inline Shape shape_of(int heads, int group, int head_dim) {
 template <int FMT, int DP, int NH, bool TOKEN_SCALES>
 cudaError_t launch(const Params& p, const Shape& s, bool join, cudaStream_t st) {
   const int warps = s.heads_per_block * s.phases;
-  const size_t smem = (size_t)warps * kStages * kStageBytes<DP>;
+  const size_t smem = (size_t)warps * kStagesOf<DP> * kStageBytes<DP>;
   auto* kernel = k_attention<FMT, DP, NH, TOKEN_SCALES>;
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(s.workers, s.groups), dim3(32 * warps), smem, st, p);
   if (e != cudaSuccess || !join) return e;
   auto* joiner = k_attention_join<DP, NH, TOKEN_SCALES>;
-  const size_t jsmem = (size_t)(kJoinWarps - 1) * s.image * 4;
-  e = ensure_dynamic_smem((const void*)joiner, jsmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(joiner, dim3(std::max(1, device_sm_count())), dim3(kJoinThreads), jsmem, st, p);
+  return launch_pdl(joiner, dim3(2 * std::max(1, device_sm_count())), dim3(kJoinThreads), 0, st, p);
 }
 
 template <int FMT, bool TOKEN_SCALES>
