@@ -82,6 +82,46 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same on a zero sum
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// four codes -> two f16 pairs (exact)
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == kE4M3) {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e5m2x2 %0, l; cvt.rn.f16x2.e5m2x2 %1, h; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float lds32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -339,7 +379,12 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   }
   const uint8_t* kbase = p.c.k + (int64_t)kvh * p.c.head_stride;
   const uint8_t* vbase = p.c.v + (int64_t)kvh * p.c.head_stride;
-  const bool tile_in_page = p.c.page_size % kAttnTile == 0;
+  // a tile lies in one page, and every piece of a row holds elements
+  const bool simple = p.c.page_size % kAttnTile == 0 && D == DP;
+  // this lane's first row and piece in a copy: its place in the cache and in a stage (a step of two
+  // copies for 128-byte rows, of one for the others, leaves the pieces' exchange as it is)
+  const int64_t lane_from = (int64_t)(lane / DPC) * p.c.token_stride + 16 * (lane % DPC);
+  const int64_t row_step = (int64_t)RPI * p.c.token_stride;
 
   for (int64_t at = t_begin; at < t_end && b < p.batch; ++b) {
     const int n = clamped_len(p, b);
@@ -357,38 +402,63 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       auto visible = [&](int tok) {
         return tok < n && (p.window == 0 || tok >= n - p.window || tok < p.sinks);
       };
+      auto all_visible = [&](int tok0) {
+        return tok0 + kAttnTile <= n && (p.window == 0 || tok0 >= n - p.window || tok0 + kAttnTile <= p.sinks);
+      };
       // page of this lane's token (lane % 16) of tile i, or -1 where nothing is to be read
       auto page_of = [&](int i) {
         if (i >= last) return -1;
-        const int tok = tile_token(i) + (tile_in_page ? 0 : (lane & 15));
+        const int tok = tile_token(i) + (simple ? 0 : (lane & 15));
         return tok < n ? __ldg(row_table + div_u32((uint32_t)tok, p.c.page_div)) : -1;
       };
       auto issue = [&](int i, int stage, int page) {
         if (i < last) {
           const int tok0 = tile_token(i);
-          const int tok = tok0 + (lane & 15);
-          const bool ok = (uint32_t)page < (uint32_t)p.c.num_pages;
-          if (!ok && visible(tok)) raise_device_error(p.err, kErrBadPage);
-          const int off = tok - (int)(div_u32((uint32_t)tok, p.c.page_div) * (uint32_t)p.c.page_size);
-          const int64_t place = ok ? (int64_t)page * p.c.page_stride + (int64_t)off * p.c.token_stride : 0;
-          const uint32_t seen = __ballot_sync(0xFFFFFFFFu, ok && visible(tok));
           const uint32_t dst = ring_u + stage * kStageBytes<DP>;
-          const int c = lane % DPC;
+          if (simple && all_visible(tok0) && (uint32_t)page < (uint32_t)p.c.num_pages) {
+            const int off = tok0 - (int)(div_u32((uint32_t)tok0, p.c.page_div) * (uint32_t)p.c.page_size);
+            const int64_t from = (int64_t)page * p.c.page_stride + (int64_t)off * p.c.token_stride + lane_from;
+            const uint8_t* k_from = kbase + from;
+            const uint8_t* v_from = vbase + from;
 #pragma unroll
-          for (int k = 0; k < kAttnTile / RPI; ++k) {
-            const int row = k * RPI + lane / DPC;
-            const int64_t from = __shfl_sync(0xFFFFFFFFu, place, row) + 16 * c;
-            const bool take = ((seen >> row) & 1u) && 16 * c < D;
-            const uint32_t to = dst + row * DP + 16 * swizzled<DP>(row, c);
-            cp_async16(to, kbase + (take ? from : 0), take);
-            cp_async16(to + kAttnTile * DP, vbase + (take ? from : 0), take);
-          }
-          if constexpr (TOKEN_SCALES) {
-            const bool take = (seen >> (lane & 15)) & 1u;
-            const int64_t slot = take ? (int64_t)page * p.c.page_size + off : 0;
-            const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
-                                                   : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
-            cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale, take);
+            for (int k = 0; k < kAttnTile / RPI; ++k) {
+              const int row = k * RPI + lane / DPC;
+              const uint32_t to = dst + row * DP + 16 * swizzled<DP>(row, lane % DPC);
+              cp_async16(to, k_from);
+              cp_async16(to + kAttnTile * DP, v_from);
+              k_from += row_step;
+              v_from += row_step;
+            }
+            if constexpr (TOKEN_SCALES) {
+              const int64_t slot = (int64_t)page * p.c.page_size + off + (lane & 15);
+              const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
+                                                     : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
+              cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale);
+            }
+          } else {
+            const int tok = tok0 + (lane & 15);
+            const bool ok = (uint32_t)page < (uint32_t)p.c.num_pages;
+            if (!ok && visible(tok)) raise_device_error(p.err, kErrBadPage);
+            const int off = tok - (int)(div_u32((uint32_t)tok, p.c.page_div) * (uint32_t)p.c.page_size);
+            const int64_t place = ok ? (int64_t)page * p.c.page_stride + (int64_t)off * p.c.token_stride : 0;
+            const uint32_t seen = __ballot_sync(0xFFFFFFFFu, ok && visible(tok));
+            const int c = lane % DPC;
+#pragma unroll 1
+            for (int k = 0; k < kAttnTile / RPI; ++k) {
+              const int row = k * RPI + lane / DPC;
+              const int64_t from = __shfl_sync(0xFFFFFFFFu, place, row) + 16 * c;
+              const bool take = ((seen >> row) & 1u) && 16 * c < D;
+              const uint32_t to = dst + row * DP + 16 * swizzled<DP>(row, c);
+              cp_async16_or_zero(to, kbase + (take ? from : 0), take);
+              cp_async16_or_zero(to + kAttnTile * DP, vbase + (take ? from : 0), take);
+            }
+            if constexpr (TOKEN_SCALES) {
+              const bool take = (seen >> (lane & 15)) & 1u;
+              const int64_t slot = take ? (int64_t)page * p.c.page_size + off : 0;
+              const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
+                                                     : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
+              cp_async4_or_zero(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale, take);
+            }
           }
         }
         cp_async_commit();
@@ -448,9 +518,9 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
           page = next;
           i_load += step;
         }
-        const uint8_t* ks = ring + stage * kStageBytes<DP>;
-        const uint8_t* vs = ks + kAttnTile * DP;
-        const float* sc = reinterpret_cast<const float*>(vs + kAttnTile * DP);
+        const uint32_t ks = ring_u + stage * kStageBytes<DP>;
+        const uint32_t vs = ks + kAttnTile * DP;
+        const uint32_t sc = vs + kAttnTile * DP;
         stage = stage == kStages - 1 ? 0 : stage + 1;
 
         // ---- S = q K^T, 16 tokens
@@ -458,51 +528,61 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc4[j][e] = 0.0f;
-          const int row = 8 * j + g;
-#pragma unroll
           for (int d = 0; d < DP / 64; ++d) {
-            const uint4 x = ld_shared_v4(ks + row * DP + 16 * swizzled<DP>(row, t + 4 * d));
+            const uint4 x = lds128(ks + g * DP + 16 * swizzled<DP>(g, t + 4 * d) + 8 * j * DP);
             const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
-              mma_f16(sc4[j], qa[0][d][2 * m], NH == 2 ? qa[NH - 1][d][2 * m] : 0u, qa[0][d][2 * m + 1],
-                      NH == 2 ? qa[NH - 1][d][2 * m + 1] : 0u, fp8x2_to_f16x2<FMT>((uint16_t)(xw[m] & 0xFFFFu)),
-                      fp8x2_to_f16x2<FMT>((uint16_t)(xw[m] >> 16)));
+            for (int m = 0; m < 4; ++m) {
+              uint32_t b0, b1;
+              decode4<FMT>(xw[m], b0, b1);
+              const uint32_t a1 = NH == 2 ? qa[NH - 1][d][2 * m] : 0u, a3 = NH == 2 ? qa[NH - 1][d][2 * m + 1] : 0u;
+              if (d == 0 && m == 0) mma_f16_first(sc4[j], qa[0][d][2 * m], a1, qa[0][d][2 * m + 1], a3, b0, b1);
+              else mma_f16(sc4[j], qa[0][d][2 * m], a1, qa[0][d][2 * m + 1], a3, b0, b1);
+            }
           }
         }
 
         // ---- softmax weights of tokens 8 j + 2 t + e, row tile h
+        float z[NH][2][2], vf[2][2], vl[2][2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float kf = 1.0f;
+            if constexpr (TOKEN_SCALES) {
+              kf = lds32(sc + 4 * (8 * j + 2 * t + e));
+              vf[j][e] = lds32(sc + 4 * (16 + 8 * j + 2 * t + e));
+              vl[j][e] = lg2(fmaxf(vf[j][e], 0x1.0p-60f));
+            }
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              z[h][j][e] = sc4[j][2 * h + e] * qmul[h];
+              if constexpr (TOKEN_SCALES) z[h][j][e] *= kf;
+            }
+          }
         const int tok0 = tile_token(i);
-        const bool whole = tok0 + kAttnTile <= n &&
-                           (p.window == 0 || tok0 >= n - p.window || tok0 + kAttnTile <= p.sinks);
-        float kf[2][2], vf[2][2], vl[2][2];
-        if constexpr (TOKEN_SCALES) {
+        if (!all_visible(tok0)) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              kf[j][e] = sc[8 * j + 2 * t + e];
-              vf[j][e] = sc[16 + 8 * j + 2 * t + e];
-              vl[j][e] = lg2(fmaxf(vf[j][e], 0x1.0p-60f));
-            }
+            for (int e = 0; e < 2; ++e)
+              if (!visible(tok0 + 8 * j + 2 * t + e)) {
+#pragma unroll
+                for (int h = 0; h < NH; ++h) z[h][j][e] = -INFINITY;
+              }
         }
         uint32_t pb[NH][2];
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          float z[2][2];
+          // V's scale counts towards the running maximum, so a weight times its scale is at most 1
+          // when it is rounded to f16
           float top = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              z[j][e] = sc4[j][2 * h + e] * qmul[h];
-              if constexpr (TOKEN_SCALES) z[j][e] *= kf[j][e];
-              if (!whole && !visible(tok0 + 8 * j + 2 * t + e)) z[j][e] = -INFINITY;
-              // V's scale counts towards the running maximum, so a weight times its scale is at
-              // most 1 when it is rounded to f16
-              if constexpr (TOKEN_SCALES) top = fmaxf(top, z[j][e] + vl[j][e]);
-              else top = fmaxf(top, z[j][e]);
+              if constexpr (TOKEN_SCALES) top = fmaxf(top, z[h][j][e] + vl[j][e]);
+              else top = fmaxf(top, z[h][j][e]);
             }
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
@@ -516,7 +596,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
           const float mr = s.m[h] == -INFINITY ? 0.0f : s.m[h];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float a = ex2(z[j][0] - mr), c = ex2(z[j][1] - mr);
+            float a = ex2(z[h][j][0] - mr), c = ex2(z[h][j][1] - mr);
             s.l[h] += a + c;
             if constexpr (TOKEN_SCALES) a *= vf[j][0], c *= vf[j][1];
             pb[h][j] = pack_f16(a, c);
@@ -528,14 +608,14 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         uint32_t v[4][VW];                   // rows 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int row = 2 * t + (k & 1) + 8 * (k >> 1);
+          const int r = 2 * t + (k & 1);
           if constexpr (DP == 64) {
-            const uint2 x = ld_shared_v2(vs + row * DP + 16 * swizzled<DP>(row, g >> 1) + 8 * (g & 1));
+            const uint2 x = lds64(vs + r * DP + 16 * swizzled<DP>(r, g >> 1) + 8 * (g & 1) + 8 * (k >> 1) * DP);
             v[k][0] = x.x, v[k][1] = x.y;
           } else {
 #pragma unroll
             for (int c = 0; c < VB / 16; ++c) {
-              const uint4 x = ld_shared_v4(vs + row * DP + 16 * swizzled<DP>(row, g * (VB / 16) + c));
+              const uint4 x = lds128(vs + r * DP + 16 * swizzled<DP>(r, g * (VB / 16) + c) + 8 * (k >> 1) * DP);
               v[k][4 * c] = x.x, v[k][4 * c + 1] = x.y, v[k][4 * c + 2] = x.z, v[k][4 * c + 3] = x.w;
             }
           }
@@ -543,17 +623,15 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
 #pragma unroll
         for (int m = 0; m < VW; ++m) {
           // bytes of both tokens side by side: dims 4 m, 4 m + 1 and 4 m + 2, 4 m + 3
-          const uint32_t x0 = __byte_perm(v[0][m], v[1][m], 0x5140), x1 = __byte_perm(v[0][m], v[1][m], 0x7362);
-          const uint32_t y0 = __byte_perm(v[2][m], v[3][m], 0x5140), y1 = __byte_perm(v[2][m], v[3][m], 0x7362);
-          const uint32_t a0 = fp8x2_to_f16x2<FMT>((uint16_t)(x0 & 0xFFFFu)), a1 = fp8x2_to_f16x2<FMT>((uint16_t)(x0 >> 16));
-          const uint32_t a2 = fp8x2_to_f16x2<FMT>((uint16_t)(y0 & 0xFFFFu)), a3 = fp8x2_to_f16x2<FMT>((uint16_t)(y0 >> 16));
-          const uint32_t c0 = fp8x2_to_f16x2<FMT>((uint16_t)(x1 & 0xFFFFu)), c1 = fp8x2_to_f16x2<FMT>((uint16_t)(x1 >> 16));
-          const uint32_t c2 = fp8x2_to_f16x2<FMT>((uint16_t)(y1 & 0xFFFFu)), c3 = fp8x2_to_f16x2<FMT>((uint16_t)(y1 >> 16));
+          uint32_t a0, a1, a2, a3;
+          decode4<FMT>(__byte_perm(v[0][m], v[1][m], 0x5140), a0, a1);
+          decode4<FMT>(__byte_perm(v[2][m], v[3][m], 0x5140), a2, a3);
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            mma_f16(s.o[h][2 * m], a0, a1, a2, a3, pb[h][0], pb[h][1]);
-            mma_f16(s.o[h][2 * m + 1], c0, c1, c2, c3, pb[h][0], pb[h][1]);
-          }
+          for (int h = 0; h < NH; ++h) mma_f16(s.o[h][2 * m], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+          decode4<FMT>(__byte_perm(v[0][m], v[1][m], 0x7362), a0, a1);
+          decode4<FMT>(__byte_perm(v[2][m], v[3][m], 0x7362), a2, a3);
+#pragma unroll
+          for (int h = 0; h < NH; ++h) mma_f16(s.o[h][2 * m + 1], a0, a1, a2, a3, pb[h][0], pb[h][1]);
         }
       }
       cp_async_wait<0>();
