@@ -13,18 +13,22 @@
 // the softmax weights are rounded to f16 (half a step is 2^-12 of a weight, below the output's
 // bf16 2^-9).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
 //
-//   S (query x token): A = q (rows g: query heads), B = K (columns: tokens)
-//   O^T (dim x query): A = V^T (rows: dims), B = P^T (columns: query heads)
+//   S^T (token x query): A = K (rows: 16 tokens), B = q (columns: 8 query heads)
+//   O^T (dim x query):   A = V^T (rows: 16 dims),  B = P^T (columns: 8 query heads)
 //
-// The result of S leaves each thread with the weights of head g = lane / 4 for tokens 2t, 2t + 1
-// (t = lane % 4), which is what B of the second product wants of it: no exchange between the two.
-// The sum's order over dims and the dims' order in O^T are free, so thread t reads 16 contiguous
-// bytes of a K row per 64 dims, and thread g head_dim / 8 contiguous bytes of a V row.
+// Both results leave a thread (g = lane / 4, t = lane % 4) with columns 2t and 2t + 1: the running
+// maximum and sum of its two heads, and the factors that rescale O, are its own.  The weights of
+// tokens g, g + 8 become the second product's operand by a transposition of 8 x 8 halves (movmatrix).
+// The order of the sum over dims and the dims' order in O^T are free, so thread t reads 16
+// contiguous bytes of a K row per 64 dims, and thread g head_dim / 8 contiguous bytes of a V row.
+// The maximum follows the scores only when one exceeds it by 2^8 (f16 holds weights to 2^16): a
+// vote a tile instead of a reduction, and next to no rescaling.
 //
 // Each warp streams the tokens of one key-value head on its own through a private ring of
-// 16-token stages (cp.async, no barrier between warps); the warps of a block take adjacent heads
-// of the same tokens, so a [token][head][dim] page is read in whole rows.  With fewer heads than
-// warps several warps take every second, third ... tile of a head and are joined in shared memory.
+// 16-token stages (cp.async, no barrier between warps), across the requests of its block's share
+// without draining; the warps of a block take adjacent heads of the same tokens, so a
+// [token][head][dim] page is read in whole rows.  With fewer heads than warps several warps take
+// every second, third ... tile of a head and are joined at a request's end through a free stage.
 //
 // All requests' tiles laid end to end are divided evenly over one wave of blocks (kv_pages.cuh), from
 // the lengths on the device: ragged batches and one long request fill the machine alike.  A
@@ -50,6 +54,7 @@ constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers s
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
 constexpr int kJoinBatch = 4;                 // parts whose loads are in flight together
+constexpr float kSlack = 8.0f;                // a score may exceed the running maximum by this (base 2)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -132,6 +137,13 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 8 x 8 f16: lane holds row lane / 4, columns 2 (lane % 4) + {0, 1}; the same of the transposed matrix
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -146,30 +158,32 @@ __device__ __forceinline__ int clamped_len(const Params& p, int b) {
   return (int)max((int64_t)0, min((int64_t)n, min((int64_t)p.max_pages * p.c.page_size, (int64_t)kMaxTokens)));
 }
 
-// Running softmax and product of one warp's query rows, as it lies in a thread's registers.
-// Row r = 8 n + lane / 4 has its maximum (base 2) and sum in m[n], l[n] (the four threads of a row
-// agree on m, and on l once reduced); o[n][i] holds dims VB g + 2 i (elements 0, 1) and
-// VB g + 2 i + 1 (elements 2, 3) of rows 8 n + 2 t and 8 n + 2 t + 1.
+// Running softmax and product of a warp's query heads, as it lies in a thread's registers: heads
+// 8 n + 2 t + e (e = 0, 1) have their reference (base 2) in m[n][e] and, over this thread's tokens
+// until reduced, their sum in l[n][e]; o[n][i] holds dims VB g + 2 i (elements e) and VB g + 2 i + 1
+// (elements 2 + e).
 template <int DP, int NH>
 struct State {
   static constexpr int kDimTiles = DP / 16;
-  float m[NH], l[NH], o[NH][kDimTiles][4];
+  // a tile of 8 heads in memory: o[i] as the float4 32 i + lane, then 8 m, then 8 l
+  static constexpr int kTileFloats = 128 * kDimTiles + 16;
+  static constexpr int kImage = NH * kTileFloats;
+  float m[NH][2], l[NH][2], o[NH][kDimTiles][4];
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
-      m[n] = -INFINITY;
-      l[n] = 0.0f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kDimTiles; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.0f;
     }
   }
-  // multiply the rows of tile n by a factor that lives in the rows' own threads
-  __device__ __forceinline__ void scale_rows(int n, float f, int lane) {
-    const int t = lane & 3;
-    const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * t), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4);
+  __device__ __forceinline__ void rescale(int n, float f0, float f1) {
+    l[n][0] *= f0;
+    l[n][1] *= f1;
 #pragma unroll
     for (int i = 0; i < kDimTiles; ++i) {
       o[n][i][0] *= f0;
@@ -178,45 +192,46 @@ struct State {
       o[n][i][3] *= f1;
     }
   }
-  // The state in memory, so that a warp's accesses are contiguous: m and l of tile n at floats
-  // 64 n + lane and 64 n + 32 + lane, then o[n][i] as the float4 32 (n kDimTiles + i) + lane.
-  static constexpr int kImage = 32 * NH * (2 + 4 * kDimTiles);
-  __device__ __forceinline__ void store(float* image, int lane) const {
+  __device__ __forceinline__ void reduce_sums() {
 #pragma unroll
-    for (int n = 0; n < NH; ++n) {
-      image[64 * n + lane] = m[n];
-      image[64 * n + 32 + lane] = l[n];
+    for (int n = 0; n < NH; ++n)
 #pragma unroll
-      for (int i = 0; i < kDimTiles; ++i)
-        reinterpret_cast<float4*>(image + 64 * NH)[32 * (n * kDimTiles + i) + lane] =
-            make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], d);
+  }
+  __device__ __forceinline__ void store_tile(int n, float* image, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kDimTiles; ++i)
+      reinterpret_cast<float4*>(image)[32 * i + lane] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+    if (lane < 4) {
+      *reinterpret_cast<float2*>(image + 128 * kDimTiles + 2 * lane) = make_float2(m[n][0], m[n][1]);
+      *reinterpret_cast<float2*>(image + 128 * kDimTiles + 8 + 2 * lane) = make_float2(l[n][0], l[n][1]);
     }
   }
-  // add a state of other tokens
-  __device__ __forceinline__ void add(const float* image, int lane) {
+  // add the heads of tile n over other tokens
+  __device__ __forceinline__ void add_tile(int n, const float* image, int lane) {
+    const float2 um = *reinterpret_cast<const float2*>(image + 128 * kDimTiles + 2 * (lane & 3));
+    const float2 ul = *reinterpret_cast<const float2*>(image + 128 * kDimTiles + 8 + 2 * (lane & 3));
+    const float m0 = fmaxf(m[n][0], um.x), m1 = fmaxf(m[n][1], um.y);
+    const float u0 = ex2_diff(um.x, m0), u1 = ex2_diff(um.y, m1);
+    rescale(n, ex2_diff(m[n][0], m0), ex2_diff(m[n][1], m1));
+    m[n][0] = m0;
+    m[n][1] = m1;
+    l[n][0] += ul.x * u0;
+    l[n][1] += ul.y * u1;
 #pragma unroll
-    for (int n = 0; n < NH; ++n) {
-      const float um = image[64 * n + lane], ul = image[64 * n + 32 + lane];
-      const float m_new = fmaxf(m[n], um);
-      const float f = ex2_diff(m[n], m_new), fu = ex2_diff(um, m_new);
-      m[n] = m_new;
-      l[n] = l[n] * f + ul * fu;
-      scale_rows(n, f, lane);
-      const int t = lane & 3;
-      const float u0 = __shfl_sync(0xFFFFFFFFu, fu, 8 * t), u1 = __shfl_sync(0xFFFFFFFFu, fu, 8 * t + 4);
-#pragma unroll
-      for (int i = 0; i < kDimTiles; ++i) {
-        const float4 x = reinterpret_cast<const float4*>(image + 64 * NH)[32 * (n * kDimTiles + i) + lane];
-        o[n][i][0] += x.x * u0;
-        o[n][i][1] += x.y * u1;
-        o[n][i][2] += x.z * u0;
-        o[n][i][3] += x.w * u1;
-      }
+    for (int i = 0; i < kDimTiles; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(image)[32 * i + lane];
+      o[n][i][0] += x.x * u0;
+      o[n][i][1] += x.y * u1;
+      o[n][i][2] += x.z * u0;
+      o[n][i][3] += x.w * u1;
     }
   }
 };
 
-// out[b][head][dim] and lse of a finished state (l reduced, V's scale applied by the caller's vs)
+// out[b][head][dim] and lse of a finished state; vs: V's scale where it is one for the head
 template <int DP, int NH>
 __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, int b, int vh, float vs, int lane) {
   constexpr int VB = DP / 8;
@@ -225,24 +240,22 @@ __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, in
   const int D = p.c.head_dim;
 #pragma unroll
   for (int n = 0; n < NH; ++n) {
-    const int row = r0 + 8 * n + g;
-    if (p.lse && t == 0 && row < p.group)
-      p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + row] =
-          s.l[n] == 0.0f ? -INFINITY : kLn2 * (s.m[n] + lg2(s.l[n]));
-    s.scale_rows(n, __fdiv_rn(vs, s.l[n]), lane);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = r0 + 8 * n + 2 * t + e;
       if (r >= p.group) continue;
+      const float l = s.l[n][e], f = __fdiv_rn(vs, l);
+      if (p.lse && g == 0)
+        p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = l == 0.0f ? -INFINITY : kLn2 * (s.m[n][e] + lg2(l));
       uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D + g * VB;
 #pragma unroll
       for (int c = 0; c < VB / 8; ++c) {
         if (g * VB + 8 * c >= D) continue;
         uint4 w;
-        w.x = f32x2_to_bf16x2(s.o[n][4 * c + 0][e], s.o[n][4 * c + 0][2 + e]);
-        w.y = f32x2_to_bf16x2(s.o[n][4 * c + 1][e], s.o[n][4 * c + 1][2 + e]);
-        w.z = f32x2_to_bf16x2(s.o[n][4 * c + 2][e], s.o[n][4 * c + 2][2 + e]);
-        w.w = f32x2_to_bf16x2(s.o[n][4 * c + 3][e], s.o[n][4 * c + 3][2 + e]);
+        w.x = f32x2_to_bf16x2(s.o[n][4 * c + 0][e] * f, s.o[n][4 * c + 0][2 + e] * f);
+        w.y = f32x2_to_bf16x2(s.o[n][4 * c + 1][e] * f, s.o[n][4 * c + 1][2 + e] * f);
+        w.z = f32x2_to_bf16x2(s.o[n][4 * c + 2][e] * f, s.o[n][4 * c + 2][2 + e] * f);
+        w.w = f32x2_to_bf16x2(s.o[n][4 * c + 3][e] * f, s.o[n][4 * c + 3][2 + e] * f);
         *reinterpret_cast<uint4*>(dst + 8 * c) = w;
       }
     }
@@ -251,7 +264,7 @@ __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, in
 
 // Position of 16-byte piece `c` of row `row` in a stage: pieces are exchanged within a row so that
 // the eight threads of a shared-memory access phase (rows g, g + 1 and pieces t of K; rows 2t and
-// pieces g, g + 1 of V) fall on different banks for 128-byte rows.
+// pieces g, g + 1 of V) fall on different banks for 128-byte rows.  Rows r and r + 8 are alike.
 template <int DP>
 __device__ __forceinline__ int swizzled(int row, int c) {
   if constexpr (DP == 64) {
@@ -263,12 +276,15 @@ __device__ __forceinline__ int swizzled(int row, int c) {
 
 template <int DP>
 constexpr int kStageBytes = 2 * kAttnTile * DP + 2 * kAttnTile * 4;
-template <int DP>
-constexpr int kStagesOf = DP == 64 ? 5 : 3;
 
 // One block per SM.  Up to 128 registers a thread 16 warps share an SM; two row tiles of 128 dims or
 // one of 256 need more, and 8 warps.
-constexpr int warps_of(int dp, int nh) { return dp * nh <= 128 ? 16 : 8; }
+__host__ __device__ constexpr int warps_of(int dp, int nh) { return dp * nh <= 128 ? 16 : 8; }
+// as many stages as fit next to one another in about 200 KB, at most 6
+__host__ __device__ constexpr int stages_of(int dp, int nh) {
+  return 204800 / (warps_of(dp, nh) * (2 * kAttnTile * dp + 2 * kAttnTile * 4)) < 6
+             ? 204800 / (warps_of(dp, nh) * (2 * kAttnTile * dp + 2 * kAttnTile * 4)) : 6;
+}
 
 // Sum over the threads up to and including this one, and over the block
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh, int64_t* all) {
@@ -290,17 +306,50 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh, int64_t* al
   return v + before;
 }
 
+// The tiles of one request that a block holds.
+struct Cursor {
+  int b;           // request; the batch size when there is none left
+  int n;           // its tokens
+  int first, end;  // its tiles [first, end) are the block's
+  int left;        // tiles of the block's share from `first` on
+  int tiles;       // all its tiles
+};
+
+__device__ __forceinline__ void enter(const Params& p, Cursor& c, int first) {
+  c.n = clamped_len(p, c.b);
+  c.tiles = attn_range(c.n, p.window, p.sinks).tiles;
+  c.first = first;
+  c.end = min(c.tiles, first + c.left);
+}
+// to the next request with tiles
+__device__ __forceinline__ void advance(const Params& p, Cursor& c) {
+  c.left -= c.end - c.first;
+  do {
+    ++c.b;
+    if (c.left <= 0) c.b = p.batch;
+    if (c.b >= p.batch) {
+      c.b = p.batch;
+      c.n = c.first = c.end = c.tiles = 0;
+      return;
+    }
+    enter(p, c, 0);
+  } while (c.tiles == 0);
+}
+
 template <int FMT, int DP, int NH, bool TOKEN_SCALES>
 __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t sh_sum[kMaxWarps];
   __shared__ int64_t sh_base;
   __shared__ int sh_req;
+  __shared__ int sh_free[kMaxWarps];         // each warp's free stage at a request's end
   constexpr int DPC = DP / 16;               // 16-byte pieces of a padded row
   constexpr int RPI = 32 / DPC;              // rows one warp-wide copy covers
   constexpr int VB = DP / 8;
-  constexpr int kStages = kStagesOf<DP>;
+  constexpr int kStages = stages_of(DP, NH);
+  constexpr int kBytes = kStageBytes<DP>;
   using St = State<DP, NH>;
+  static_assert(St::kTileFloats * 4 <= kBytes, "a stage holds the state of 8 heads");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -312,26 +361,29 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   const int D = p.c.head_dim;
 
   if (threadIdx.x == 0) sh_req = p.batch;
+  if (p.batch > 0) prefetch_l2(p.lens + min((int)threadIdx.x, p.batch - 1));
   allow_dependent_launch();
   grid_dependency_wait();
 
   // ---- total number of tiles; this block's share of them, and the request it begins in.  With at
-  // most one request a thread one sum over the block gives both.
+  // most one request a thread one sum over the block gives all.  Requests without a visible token
+  // are counted from bit 48 on.
+  constexpr int64_t kOneEmpty = int64_t(1) << 48;
   const bool single = p.batch <= (int)blockDim.x;
-  int64_t tiles = 0, total = 0, upto = 0;
-  bool empty = false;
+  int64_t mine = 0;
   for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
     const int n = attn_range(clamped_len(p, b), p.window, p.sinks).tiles;
-    tiles += n;
-    empty |= n == 0;
+    mine += n == 0 ? kOneEmpty : n;
   }
-  upto = block_sum(tiles, sh_sum, &total);
+  int64_t all;
+  const int64_t upto = block_sum(mine, sh_sum, &all) & (kOneEmpty - 1);
+  const int64_t total = all & (kOneEmpty - 1);
   const int workers = attn_workers(total, p.workers, kMinTiles);
   const int w = blockIdx.x;
   if (blockIdx.y == 0 && threadIdx.x == 0 && p.desc) p.desc[w] = make_int4(-1, 0, 0, 0);
 
   // requests without a visible token: zeros, and an empty sum
-  if (__syncthreads_or(empty)) {
+  if (all >= kOneEmpty) {
     for (int b = w; b < p.batch; b += p.workers) {
       if (clamped_len(p, b) > 0) continue;
       if (active && phase == 0) {
@@ -346,6 +398,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   if (w >= workers || total == 0) return;
   const int64_t t_begin = attn_start(total, workers, w), t_end = attn_start(total, workers, w + 1);
   if (single) {
+    const int64_t tiles = mine & (kOneEmpty - 1);
     if (tiles > 0 && upto - tiles <= t_begin && t_begin < upto) {
       sh_req = threadIdx.x;
       sh_base = upto - tiles;
@@ -355,7 +408,6 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
     for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
       const int b = b0 + threadIdx.x;
       const int64_t n = b < p.batch ? attn_range(clamped_len(p, b), p.window, p.sinks).tiles : 0;
-      int64_t all;
       const int64_t incl = before + block_sum(n, sh_sum, &all);
       if (n > 0 && incl - n <= t_begin && t_begin < incl) {
         sh_req = b;
@@ -365,12 +417,15 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       if (before > t_begin) break;           // the same for every thread
     }
   }
+  const uint32_t ring_u = smem_u32(smem) + (uint32_t)warp * (kStages * kBytes);
+  if (D < DP) {
+    // the pieces past head_dim stay zero: no copy writes them
+    for (int i = lane; i < kStages * kBytes / 16; i += 32)
+      *reinterpret_cast<uint4*>(smem + (size_t)warp * (kStages * kBytes) + 16 * i) = make_uint4(0, 0, 0, 0);
+  }
   __syncthreads();
-  int b = sh_req;
-  int64_t base = sh_base;
+  if (!active || sh_req >= p.batch) return;
 
-  uint8_t* ring = smem + (size_t)warp * (kStages * kStageBytes<DP>);
-  const uint32_t ring_u = smem_u32(ring);
   float vscale = 1.0f, kscale = 1.0f;
   if constexpr (!TOKEN_SCALES) {
     const int i = p.c.gran == 0 ? 0 : kvh;
@@ -379,297 +434,321 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   }
   const uint8_t* kbase = p.c.k + (int64_t)kvh * p.c.head_stride;
   const uint8_t* vbase = p.c.v + (int64_t)kvh * p.c.head_stride;
-  // a tile lies in one page, and every piece of a row holds elements
-  const bool simple = p.c.page_size % kAttnTile == 0 && D == DP;
-  // this lane's first row and piece in a copy: its place in the cache and in a stage (a step of two
-  // copies for 128-byte rows, of one for the others, leaves the pieces' exchange as it is)
-  const int64_t lane_from = (int64_t)(lane / DPC) * p.c.token_stride + 16 * (lane % DPC);
-  const int64_t row_step = (int64_t)RPI * p.c.token_stride;
+  const bool tile_in_page = p.c.page_size % kAttnTile == 0;
+  const int row0 = lane / DPC, piece = lane % DPC;                 // this lane's first row and its piece in a copy
+  const bool has_piece = 16 * piece < D;
+  const uint32_t token16 = (uint32_t)(p.c.token_stride / 16), page16 = (uint32_t)(p.c.page_stride / 16);
 
-  for (int64_t at = t_begin; at < t_end && b < p.batch; ++b) {
-    const int n = clamped_len(p, b);
-    const AttnRange range = attn_range(n, p.window, p.sinks);
-    if (range.tiles == 0) continue;
-    const int first = (int)(at - base);
-    const int last = (int)min((int64_t)range.tiles, t_end - base);   // one past this block's last tile
+  Cursor load, c;                            // of the copies, and of the products
+  c.b = sh_req;
+  c.left = (int)(t_end - t_begin);
+  enter(p, c, (int)(t_begin - sh_base));
+  load = c;
+
+  auto tile_token = [&](int i, int n) {
+    if (p.window > 0) {
+      const AttnRange r = attn_range(n, p.window, p.sinks);
+      if (i >= r.head) i += r.skip;
+    }
+    return i * kAttnTile;
+  };
+  auto visible = [&](int tok, int n) { return tok < n && (p.window == 0 || tok >= n - p.window || tok < p.sinks); };
+  auto all_visible = [&](int tok0, int n) {
+    return tok0 + kAttnTile <= n && (p.window == 0 || tok0 >= n - p.window || tok0 + kAttnTile <= p.sinks);
+  };
+  auto prefetch_q = [&](int b) {
+    const int bytes = min(8 * NH, p.group - r0) * D * 2;
+    if (lane * 128 < bytes)
+      prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + r0) * D) + lane * 128);
+  };
+
+  // ---- copies: `i_load` is the next tile to copy, `page` the page of this lane's token of it
+  // (lane % 16, or the tile's) or -1 where there is none
+  int i_load = load.first + phase, page = -1, tok_load = 0;
+  auto find_page = [&]() {
+    while (i_load >= load.end && load.b < p.batch) {
+      advance(p, load);
+      i_load = load.first + phase;
+      if (load.b < p.batch) prefetch_q(load.b);
+    }
+    page = -1;
+    if (load.b >= p.batch) return;
+    tok_load = tile_token(i_load, load.n);
+    const int tok = tok_load + (tile_in_page ? 0 : (lane & 15));
+    if (tok < load.n) page = __ldg(p.table + (int64_t)load.b * p.max_pages + div_u32((uint32_t)tok, p.c.page_div));
+  };
+  auto issue = [&](int slot_index) {
+    if (load.b < p.batch) {
+      const uint32_t dst = ring_u + slot_index * kBytes;
+      const bool whole = all_visible(tok_load, load.n);
+      if (tile_in_page && whole && (uint32_t)page < (uint32_t)p.c.num_pages) {
+        const int off = tok_load - (int)(div_u32((uint32_t)tok_load, p.c.page_div) * (uint32_t)p.c.page_size);
+        if (has_piece) {
+          // places in units of 16 bytes fit 32 bits (checked on the host)
+          uint32_t at = (uint32_t)page * page16 + (uint32_t)(off + row0) * token16 + piece;
+#pragma unroll
+          for (int k = 0; k < kAttnTile / RPI; ++k) {
+            const uint32_t to = dst + row0 * DP + 16 * swizzled<DP>(k * RPI + row0, piece) + k * RPI * DP;
+            cp_async16(to, kbase + (uint64_t)at * 16);
+            cp_async16(to + kAttnTile * DP, vbase + (uint64_t)at * 16);
+            at += RPI * token16;
+          }
+        }
+        if constexpr (TOKEN_SCALES) {
+          const int64_t slot = (int64_t)page * p.c.page_size + off + (lane & 15);
+          const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
+                                                 : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
+          cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale);
+        }
+      } else {
+        const int tok = tok_load + (lane & 15);
+        const bool ok = (uint32_t)page < (uint32_t)p.c.num_pages;
+        const bool see = visible(tok, load.n);
+        if (!ok && see) raise_device_error(p.err, kErrBadPage);
+        const int off = tok - (int)(div_u32((uint32_t)tok, p.c.page_div) * (uint32_t)p.c.page_size);
+        const uint32_t place = (uint32_t)page * page16 + (uint32_t)off * token16;
+        const uint32_t seen = __ballot_sync(0xFFFFFFFFu, ok && see);
+#pragma unroll
+        for (int k = 0; k < kAttnTile / RPI; ++k) {
+          const int row = k * RPI + row0;
+          const uint32_t at = __shfl_sync(0xFFFFFFFFu, place, row) + piece;
+          const bool take = (seen >> row) & 1u;
+          const uint64_t from = take ? (uint64_t)at * 16 : 0;
+          const uint32_t to = dst + row0 * DP + 16 * swizzled<DP>(k * RPI + row0, piece) + k * RPI * DP;
+          if (has_piece) {
+            cp_async16_or_zero(to, kbase + from, take);
+            cp_async16_or_zero(to + kAttnTile * DP, vbase + from, take);
+          }
+        }
+        if constexpr (TOKEN_SCALES) {
+          const bool take = (seen >> (lane & 15)) & 1u;
+          const int64_t slot = take ? (int64_t)page * p.c.page_size + off : 0;
+          const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
+                                                 : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
+          cp_async4_or_zero(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale, take);
+        }
+      }
+      i_load += p.phases;
+    }
+    cp_async_commit();
+  };
+
+  prefetch_q(c.b);
+  find_page();
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) {
+    issue(k);
+    find_page();
+  }
+  int stage = 0;                             // the next stage to be read; the one before it is free
+
+  while (c.b < p.batch) {
+    const int b = c.b, n = c.n;
+    // ---- query heads as B fragments: f16 after a power of two that brings a head's largest element to
+    // 2^14 .. 2^15; the inverse power joins the score's factor
+    uint32_t qb[NH][DP / 64][8];
+    float qmul[NH][2];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int r = r0 + 8 * h + g;
+      const uint16_t* src = p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + min(r, p.group - 1)) * D;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int j = 0; j < DP / 64; ++j) {
+        const int k = t + 4 * j;
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (r < p.group && 16 * k < D) {
+          x = __ldg(reinterpret_cast<const uint4*>(src + 16 * k));
+          y = __ldg(reinterpret_cast<const uint4*>(src + 16 * k + 8));
+        }
+        qb[h][j][0] = x.x, qb[h][j][1] = x.y, qb[h][j][2] = x.z, qb[h][j][3] = x.w;
+        qb[h][j][4] = y.x, qb[h][j][5] = y.y, qb[h][j][6] = y.z, qb[h][j][7] = y.w;
+        mx = absmax_v4(absmax_v4(mx, x), y);
+      }
+      mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+      mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+      const uint32_t ex = __float_as_uint(packed_amax_to_f32(mx)) >> 23;   // biased exponent of the largest
+      const uint32_t up = ex == 255u ? 127u : min(268u - ex, 253u);
+      const float f = __uint_as_float(up << 23);
+      const float back = __uint_as_float((254u - up) << 23) * p.scale2 * kscale;
+      qmul[h][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
+      qmul[h][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
+#pragma unroll
+      for (int j = 0; j < DP / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) qb[h][j][i] = pack_f16(bf16_lo(qb[h][j][i]) * f, bf16_hi(qb[h][j][i]) * f);
+    }
+
     St s;
     s.clear();
+    for (int i = c.first + phase; i < c.end; i += p.phases) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();                          // the stage has landed for every lane; the one before is read out
+      issue(stage == 0 ? kStages - 1 : stage - 1);
+      find_page();
+      const uint32_t ks = ring_u + stage * kBytes;
+      const uint32_t vs = ks + kAttnTile * DP;
+      const uint32_t sc = vs + kAttnTile * DP;
+      stage = stage == kStages - 1 ? 0 : stage + 1;
 
-    if (active) {
-      const int* row_table = p.table + (int64_t)b * p.max_pages;
-      // token of tile i's first row
-      auto tile_token = [&](int i) { return (i < range.head ? i : i + range.skip) * kAttnTile; };
-      auto visible = [&](int tok) {
-        return tok < n && (p.window == 0 || tok >= n - p.window || tok < p.sinks);
-      };
-      auto all_visible = [&](int tok0) {
-        return tok0 + kAttnTile <= n && (p.window == 0 || tok0 >= n - p.window || tok0 + kAttnTile <= p.sinks);
-      };
-      // page of this lane's token (lane % 16) of tile i, or -1 where nothing is to be read
-      auto page_of = [&](int i) {
-        if (i >= last) return -1;
-        const int tok = tile_token(i) + (simple ? 0 : (lane & 15));
-        return tok < n ? __ldg(row_table + div_u32((uint32_t)tok, p.c.page_div)) : -1;
-      };
-      auto issue = [&](int i, int stage, int page) {
-        if (i < last) {
-          const int tok0 = tile_token(i);
-          const uint32_t dst = ring_u + stage * kStageBytes<DP>;
-          if (simple && all_visible(tok0) && (uint32_t)page < (uint32_t)p.c.num_pages) {
-            const int off = tok0 - (int)(div_u32((uint32_t)tok0, p.c.page_div) * (uint32_t)p.c.page_size);
-            const int64_t from = (int64_t)page * p.c.page_stride + (int64_t)off * p.c.token_stride + lane_from;
-            const uint8_t* k_from = kbase + from;
-            const uint8_t* v_from = vbase + from;
+      // ---- S^T = K q^T: elements 0, 1 are token g, elements 2, 3 token g + 8
+      float st[NH][4];
 #pragma unroll
-            for (int k = 0; k < kAttnTile / RPI; ++k) {
-              const int row = k * RPI + lane / DPC;
-              const uint32_t to = dst + row * DP + 16 * swizzled<DP>(row, lane % DPC);
-              cp_async16(to, k_from);
-              cp_async16(to + kAttnTile * DP, v_from);
-              k_from += row_step;
-              v_from += row_step;
-            }
-            if constexpr (TOKEN_SCALES) {
-              const int64_t slot = (int64_t)page * p.c.page_size + off + (lane & 15);
-              const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
-                                                     : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
-              cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale);
-            }
-          } else {
-            const int tok = tok0 + (lane & 15);
-            const bool ok = (uint32_t)page < (uint32_t)p.c.num_pages;
-            if (!ok && visible(tok)) raise_device_error(p.err, kErrBadPage);
-            const int off = tok - (int)(div_u32((uint32_t)tok, p.c.page_div) * (uint32_t)p.c.page_size);
-            const int64_t place = ok ? (int64_t)page * p.c.page_stride + (int64_t)off * p.c.token_stride : 0;
-            const uint32_t seen = __ballot_sync(0xFFFFFFFFu, ok && visible(tok));
-            const int c = lane % DPC;
-#pragma unroll 1
-            for (int k = 0; k < kAttnTile / RPI; ++k) {
-              const int row = k * RPI + lane / DPC;
-              const int64_t from = __shfl_sync(0xFFFFFFFFu, place, row) + 16 * c;
-              const bool take = ((seen >> row) & 1u) && 16 * c < D;
-              const uint32_t to = dst + row * DP + 16 * swizzled<DP>(row, c);
-              cp_async16_or_zero(to, kbase + (take ? from : 0), take);
-              cp_async16_or_zero(to + kAttnTile * DP, vbase + (take ? from : 0), take);
-            }
-            if constexpr (TOKEN_SCALES) {
-              const bool take = (seen >> (lane & 15)) & 1u;
-              const int64_t slot = take ? (int64_t)page * p.c.page_size + off : 0;
-              const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
-                                                     : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
-              cp_async4_or_zero(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale, take);
-            }
+      for (int d = 0; d < DP / 64; ++d) {
+        const uint32_t at = ks + g * DP + 16 * swizzled<DP>(g, t + 4 * d);
+        const uint4 x = lds128(at), y = lds128(at + 8 * DP);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          uint32_t a0, a1, a2, a3;
+          decode4<FMT>(xw[m], a0, a2);
+          decode4<FMT>(yw[m], a1, a3);
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            if (d == 0 && m == 0) mma_f16_first(st[h], a0, a1, a2, a3, qb[h][d][2 * m], qb[h][d][2 * m + 1]);
+            else mma_f16(st[h], a0, a1, a2, a3, qb[h][d][2 * m], qb[h][d][2 * m + 1]);
           }
         }
-        cp_async_commit();
-      };
-
-      const int step = p.phases;
-      int i_load = first + phase;
-      int page = page_of(i_load);
-#pragma unroll
-      for (int k = 0; k < kStages - 1; ++k) {
-        const int next = page_of(i_load + step);
-        issue(i_load, k, page);
-        page = next;
-        i_load += step;
-      }
-      // ---- query rows as A fragments: f16 after a power of two that brings the row's largest
-      // element to 2^14 .. 2^15; the inverse power joins the score's factor
-      uint32_t qa[NH][DP / 64][8];
-      float qmul[NH];
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        const int r = r0 + 8 * h + g;
-        const uint16_t* src = p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + min(r, p.group - 1)) * D;
-        uint32_t raw[DP / 64][8];
-        uint32_t mx = 0;
-#pragma unroll
-        for (int j = 0; j < DP / 64; ++j) {
-          const int c = t + 4 * j;
-          uint4 x = make_uint4(0, 0, 0, 0), y = x;
-          if (r < p.group && 16 * c < D) {
-            x = __ldg(reinterpret_cast<const uint4*>(src + 16 * c));
-            y = __ldg(reinterpret_cast<const uint4*>(src + 16 * c + 8));
-          }
-          raw[j][0] = x.x, raw[j][1] = x.y, raw[j][2] = x.z, raw[j][3] = x.w;
-          raw[j][4] = y.x, raw[j][5] = y.y, raw[j][6] = y.z, raw[j][7] = y.w;
-          mx = absmax_v4(absmax_v4(mx, x), y);
-        }
-        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-        mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        const uint32_t ex = __float_as_uint(packed_amax_to_f32(mx)) >> 23;   // biased exponent of the largest
-        const uint32_t up = ex == 255u ? 127u : min(268u - ex, 253u);
-        const float f = __uint_as_float(up << 23);
-        qmul[h] = __uint_as_float((254u - up) << 23) * p.scale2 * kscale;
-#pragma unroll
-        for (int j = 0; j < DP / 64; ++j)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) qa[h][j][i] = pack_f16(bf16_lo(raw[j][i]) * f, bf16_hi(raw[j][i]) * f);
       }
 
-      int stage = 0;
-      for (int i = first + phase; i < last; i += step) {
-        cp_async_wait<kStages - 2>();
-        __syncwarp();                        // the stage has landed for every lane; the one before is read out
-        {
-          const int next = page_of(i_load + step);
-          issue(i_load, stage == 0 ? kStages - 1 : stage - 1, page);
-          page = next;
-          i_load += step;
-        }
-        const uint32_t ks = ring_u + stage * kStageBytes<DP>;
-        const uint32_t vs = ks + kAttnTile * DP;
-        const uint32_t sc = vs + kAttnTile * DP;
-        stage = stage == kStages - 1 ? 0 : stage + 1;
-
-        // ---- S = q K^T, 16 tokens
-        float sc4[2][4];
+      // ---- softmax weights
+      float vf[2], vl[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+      for (int h = 0; h < NH; ++h)
 #pragma unroll
-          for (int d = 0; d < DP / 64; ++d) {
-            const uint4 x = lds128(ks + g * DP + 16 * swizzled<DP>(g, t + 4 * d) + 8 * j * DP);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+        for (int e = 0; e < 4; ++e) st[h][e] *= qmul[h][e & 1];
+      if constexpr (TOKEN_SCALES) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              uint32_t b0, b1;
-              decode4<FMT>(xw[m], b0, b1);
-              const uint32_t a1 = NH == 2 ? qa[NH - 1][d][2 * m] : 0u, a3 = NH == 2 ? qa[NH - 1][d][2 * m + 1] : 0u;
-              if (d == 0 && m == 0) mma_f16_first(sc4[j], qa[0][d][2 * m], a1, qa[0][d][2 * m + 1], a3, b0, b1);
-              else mma_f16(sc4[j], qa[0][d][2 * m], a1, qa[0][d][2 * m + 1], a3, b0, b1);
-            }
+        for (int k = 0; k < 2; ++k) {
+          const float kf = lds32(sc + 4 * (g + 8 * k));
+          vf[k] = lds32(sc + 4 * (16 + g + 8 * k));
+          vl[k] = lg2(fmaxf(vf[k], 0x1.0p-60f));
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            st[h][2 * k] *= kf;
+            st[h][2 * k + 1] *= kf;
           }
         }
-
-        // ---- softmax weights of tokens 8 j + 2 t + e, row tile h
-        float z[NH][2][2], vf[2][2], vl[2][2];
+      }
+      const int tok0 = tile_token(i, n);
+      if (!all_visible(tok0, n)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int k = 0; k < 2; ++k)
+          if (!visible(tok0 + g + 8 * k, n)) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float kf = 1.0f;
-            if constexpr (TOKEN_SCALES) {
-              kf = lds32(sc + 4 * (8 * j + 2 * t + e));
-              vf[j][e] = lds32(sc + 4 * (16 + 8 * j + 2 * t + e));
-              vl[j][e] = lg2(fmaxf(vf[j][e], 0x1.0p-60f));
-            }
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-              z[h][j][e] = sc4[j][2 * h + e] * qmul[h];
-              if constexpr (TOKEN_SCALES) z[h][j][e] *= kf;
-            }
+            for (int h = 0; h < NH; ++h) st[h][2 * k] = st[h][2 * k + 1] = -INFINITY;
           }
-        const int tok0 = tile_token(i);
-        if (!all_visible(tok0)) {
+      }
+      // V's scale counts towards the reference, so that a weight times its scale fits f16
+      bool above = false;
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+      for (int h = 0; h < NH; ++h)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!visible(tok0 + 8 * j + 2 * t + e)) {
-#pragma unroll
-                for (int h = 0; h < NH; ++h) z[h][j][e] = -INFINITY;
-              }
-        }
-        uint32_t pb[NH][2];
+        for (int e = 0; e < 4; ++e) above |= (TOKEN_SCALES ? st[h][e] + vl[e >> 1] : st[h][e]) > s.m[h][e & 1] + kSlack;
+      if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          // V's scale counts towards the running maximum, so a weight times its scale is at most 1
-          // when it is rounded to f16
-          float top = -INFINITY;
+          float top[2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int e = 0; e < 2; ++e) {
+            top[e] = TOKEN_SCALES ? fmaxf(st[h][e] + vl[0], st[h][2 + e] + vl[1]) : fmaxf(st[h][e], st[h][2 + e]);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              if constexpr (TOKEN_SCALES) top = fmaxf(top, z[h][j][e] + vl[j][e]);
-              else top = fmaxf(top, z[h][j][e]);
-            }
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          if (__any_sync(0xFFFFFFFFu, top > s.m[h])) {
-            const float m_new = fmaxf(s.m[h], top);
-            const float f = m_new == -INFINITY ? 1.0f : ex2(s.m[h] - m_new);
-            s.m[h] = m_new;
-            s.l[h] *= f;
-            s.scale_rows(h, f, lane);
+            for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], d));
+            top[e] = fmaxf(top[e], s.m[h][e]);
           }
-          const float mr = s.m[h] == -INFINITY ? 0.0f : s.m[h];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float a = ex2(z[h][j][0] - mr), c = ex2(z[h][j][1] - mr);
-            s.l[h] += a + c;
-            if constexpr (TOKEN_SCALES) a *= vf[j][0], c *= vf[j][1];
-            pb[h][j] = pack_f16(a, c);
-          }
-        }
-
-        // ---- O^T += V^T P^T
-        constexpr int VW = VB / 4;           // words of a row a thread reads
-        uint32_t v[4][VW];                   // rows 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 2 * t + (k & 1);
-          if constexpr (DP == 64) {
-            const uint2 x = lds64(vs + r * DP + 16 * swizzled<DP>(r, g >> 1) + 8 * (g & 1) + 8 * (k >> 1) * DP);
-            v[k][0] = x.x, v[k][1] = x.y;
-          } else {
-#pragma unroll
-            for (int c = 0; c < VB / 16; ++c) {
-              const uint4 x = lds128(vs + r * DP + 16 * swizzled<DP>(r, g * (VB / 16) + c) + 8 * (k >> 1) * DP);
-              v[k][4 * c] = x.x, v[k][4 * c + 1] = x.y, v[k][4 * c + 2] = x.z, v[k][4 * c + 3] = x.w;
-            }
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < VW; ++m) {
-          // bytes of both tokens side by side: dims 4 m, 4 m + 1 and 4 m + 2, 4 m + 3
-          uint32_t a0, a1, a2, a3;
-          decode4<FMT>(__byte_perm(v[0][m], v[1][m], 0x5140), a0, a1);
-          decode4<FMT>(__byte_perm(v[2][m], v[3][m], 0x5140), a2, a3);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) mma_f16(s.o[h][2 * m], a0, a1, a2, a3, pb[h][0], pb[h][1]);
-          decode4<FMT>(__byte_perm(v[0][m], v[1][m], 0x7362), a0, a1);
-          decode4<FMT>(__byte_perm(v[2][m], v[3][m], 0x7362), a2, a3);
-#pragma unroll
-          for (int h = 0; h < NH; ++h) mma_f16(s.o[h][2 * m + 1], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+          s.rescale(h, ex2_diff(s.m[h][0], top[0]), ex2_diff(s.m[h][1], top[1]));
+          s.m[h][0] = top[0];
+          s.m[h][1] = top[1];
         }
       }
-      cp_async_wait<0>();
+      uint32_t pb[NH][2];
 #pragma unroll
       for (int h = 0; h < NH; ++h) {
-        s.l[h] += __shfl_xor_sync(0xFFFFFFFFu, s.l[h], 1);
-        s.l[h] += __shfl_xor_sync(0xFFFFFFFFu, s.l[h], 2);
+        const float m0 = s.m[h][0] == -INFINITY ? 0.0f : s.m[h][0], m1 = s.m[h][1] == -INFINITY ? 0.0f : s.m[h][1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float a = ex2(st[h][2 * k] - m0), e = ex2(st[h][2 * k + 1] - m1);
+          s.l[h][0] += a;
+          s.l[h][1] += e;
+          if constexpr (TOKEN_SCALES) a *= vf[k], e *= vf[k];
+          pb[h][k] = transpose8(pack_f16(a, e));
+        }
       }
-      __syncwarp();                          // every lane has read the last stages
+
+      // ---- O^T += V^T P^T
+      constexpr int VW = VB / 4;             // words of a row a thread reads
+      uint32_t v[4][VW];                     // rows 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = 2 * t + (k & 1);
+        if constexpr (DP == 64) {
+          const uint2 x = lds64(vs + r * DP + 16 * swizzled<DP>(r, g >> 1) + 8 * (g & 1) + 8 * (k >> 1) * DP);
+          v[k][0] = x.x, v[k][1] = x.y;
+        } else {
+#pragma unroll
+          for (int e = 0; e < VB / 16; ++e) {
+            const uint4 x = lds128(vs + r * DP + 16 * swizzled<DP>(r, g * (VB / 16) + e) + 8 * (k >> 1) * DP);
+            v[k][4 * e] = x.x, v[k][4 * e + 1] = x.y, v[k][4 * e + 2] = x.z, v[k][4 * e + 3] = x.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < VW; ++m) {
+        // bytes of both tokens side by side: dims 4 m, 4 m + 1 and 4 m + 2, 4 m + 3
+        uint32_t a0, a1, a2, a3;
+        decode4<FMT>(__byte_perm(v[0][m], v[1][m], 0x5140), a0, a1);
+        decode4<FMT>(__byte_perm(v[2][m], v[3][m], 0x5140), a2, a3);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) mma_f16(s.o[h][2 * m], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+        decode4<FMT>(__byte_perm(v[0][m], v[1][m], 0x7362), a0, a1);
+        decode4<FMT>(__byte_perm(v[2][m], v[3][m], 0x7362), a2, a3);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) mma_f16(s.o[h][2 * m + 1], a0, a1, a2, a3, pb[h][0], pb[h][1]);
+      }
     }
 
-    // ---- warps that shared a head's tiles: the first adds up the others' states
+    // ---- the request's end: warps that shared a head's tiles meet, and the first adds up the others'
+    // states from their free stages
+    s.reduce_sums();
     if (p.phases > 1) {
-      __syncthreads();
-      if (active && phase > 0) s.store(reinterpret_cast<float*>(ring), lane);
-      __syncthreads();
-      if (active && phase == 0)
-        for (int k = 1; k < p.phases; ++k)
-          s.add(reinterpret_cast<const float*>(smem + (size_t)(warp + k * p.heads_per_block) * (kStages * kStageBytes<DP>)),
-                lane);
-      __syncthreads();                       // the images are read before the ring is filled again
+      const uint32_t bar = 1 + warp % p.heads_per_block, threads = 32 * p.phases;
+      const int free_stage = stage == 0 ? kStages - 1 : stage - 1;
+      uint8_t* mine_at = smem + (size_t)warp * (kStages * kBytes) + free_stage * kBytes;
+      if (lane == 0) sh_free[warp] = free_stage;
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        __syncwarp();                        // every lane has read the stage
+        if (phase > 0) s.store_tile(h, reinterpret_cast<float*>(mine_at), lane);
+        named_barrier(bar, threads);
+        if (phase == 0)
+          for (int k = 1; k < p.phases; ++k) {
+            const int other = warp + k * p.heads_per_block;
+            s.add_tile(h, reinterpret_cast<const float*>(smem + ((size_t)other * kStages + sh_free[other]) * kBytes), lane);
+          }
+        named_barrier(bar, threads);         // the stages are read before they are written again
+      }
+      if (D < DP && phase > 0) {
+        // the free stage's pieces past head_dim are zero again
+        for (int i = lane; i < kBytes / 16; i += 32) reinterpret_cast<uint4*>(mine_at)[i] = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
     }
-
-    if (active && phase == 0) {
-      if (first == 0 && last == range.tiles) {
+    const bool opens = c.first == 0, closes = c.end == c.tiles;
+    const int place = c.left == (int)(t_end - t_begin) ? 0 : 1;    // the block's first request, or a later one
+    if (phase == 0) {
+      if (opens && closes) {
         write_rows<DP, NH>(p, s, b, vh, vscale, lane);
       } else {
-        // a request's part that begins where this block's range begins goes to place 0, else to 1
-        const int place = at == t_begin ? 0 : 1;
-        s.store(p.part + ((int64_t)(2 * w + place) * p.vheads + vh) * St::kImage, lane);
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          s.store_tile(h, p.part + ((int64_t)(2 * w + place) * p.vheads + vh) * St::kImage + h * St::kTileFloats, lane);
       }
     }
-    if (first == 0 && last < range.tiles && blockIdx.y == 0 && threadIdx.x == 0)
-      p.desc[w] = make_int4(b, at == t_begin ? 0 : 1, w,
-                            min(workers - 1, attn_owner(total, workers, base + range.tiles - 1)));
-    base += range.tiles;
-    at = base < t_end ? base : t_end;
+    if (opens && !closes && blockIdx.y == 0 && threadIdx.x == 0)
+      p.desc[w] = make_int4(b, place, w, min(workers - 1, attn_owner(total, workers, t_end - c.left + c.tiles - 1)));
+    advance(p, c);
   }
+  cp_async_wait<0>();
 }
 
 // Second launch: adds up the parts of each shared request.  A unit is a quarter of a part of 128
@@ -725,7 +804,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
       e = list[v / p.vheads];
       n = part / kPairs;
       pair = part % kPairs;
-      // rows 2t and 2t + 1 have their maximum and sum in lanes 8t and 8t + 4 of the image
       for (int x0 = e.z + mine; x0 <= e.w; x0 += wpu * kJoinBatch) {
         float um[kJoinBatch][2], ul[kJoinBatch][2];
         float4 uo[kJoinBatch][2];
@@ -736,12 +814,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
           ul[k][0] = ul[k][1] = 0.0f;
           uo[k][0] = uo[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if (x <= e.w) {
-            const float* image = p.part + ((int64_t)(2 * x + (x == e.z ? e.y : 0)) * p.vheads + vh) * St::kImage;
-            um[k][0] = image[64 * n + 8 * t];
-            um[k][1] = image[64 * n + 8 * t + 4];
-            ul[k][0] = image[64 * n + 32 + 8 * t];
-            ul[k][1] = image[64 * n + 32 + 8 * t + 4];
-            const float4* q = reinterpret_cast<const float4*>(image + 64 * NH) + 32 * (n * St::kDimTiles + 2 * pair) + lane;
+            const float* image = p.part + ((int64_t)(2 * x + (x == e.z ? e.y : 0)) * p.vheads + vh) * St::kImage +
+                                 n * St::kTileFloats;
+            const float2 xm = *reinterpret_cast<const float2*>(image + 128 * St::kDimTiles + 2 * t);
+            const float2 xl = *reinterpret_cast<const float2*>(image + 128 * St::kDimTiles + 8 + 2 * t);
+            um[k][0] = xm.x, um[k][1] = xm.y;
+            ul[k][0] = xl.x, ul[k][1] = xl.y;
+            const float4* q = reinterpret_cast<const float4*>(image) + 64 * pair + lane;
             uo[k][0] = q[0];
             uo[k][1] = q[32];
           }
@@ -827,14 +906,14 @@ inline Shape shape_of(int heads, int group, int head_dim) {
   s.heads_per_block = (s.vheads + s.groups - 1) / s.groups;
   s.phases = warps / s.heads_per_block;
   s.workers = std::min(kMaxWorkers, std::max(1, device_sm_count() / s.groups));
-  s.image = 32 * s.nh * (s.dp / 4 + 2);
+  s.image = s.nh * (8 * s.dp + 16);
   return s;
 }
 
 template <int FMT, int DP, int NH, bool TOKEN_SCALES>
 cudaError_t launch(const Params& p, const Shape& s, bool join, cudaStream_t st) {
   const int warps = s.heads_per_block * s.phases;
-  const size_t smem = (size_t)warps * kStagesOf<DP> * kStageBytes<DP>;
+  const size_t smem = (size_t)warps * stages_of(DP, NH) * kStageBytes<DP>;
   auto* kernel = k_attention<FMT, DP, NH, TOKEN_SCALES>;
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e != cudaSuccess) return e;

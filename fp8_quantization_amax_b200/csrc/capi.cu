@@ -37,6 +37,8 @@ int64_t checked_elems(int64_t a, int64_t b) {
 
 constexpr int64_t kMaxTableTokens = (int64_t(1) << 31) - 65;   // token numbers and slots fit an int
 
+constexpr int64_t kMaxSpan = int64_t(1) << 36;                 // bytes of a paged K or V
+
 // A paged cache from the caller's description; FP8Q_OK and *out, or the reason why not.
 fp8q_status paged_cache(const fp8q_kv_pages* c, fp8q::KvPages* out) {
   if (!c || !valid_fmt(c->f) || c->g < FP8Q_KV_PER_TENSOR || c->g > FP8Q_KV_PER_TOKEN) return FP8Q_ERR_INVALID_ARGUMENT;
@@ -45,6 +47,11 @@ fp8q_status paged_cache(const fp8q_kv_pages* c, fp8q::KvPages* out) {
     return FP8Q_ERR_INVALID_ARGUMENT;
   if (c->head_dim > 256 || c->heads > 65536 || c->page_size > kMaxTableTokens ||
       (c->num_pages > 0 && c->page_size > kMaxTableTokens / c->num_pages))
+    return FP8Q_ERR_UNSUPPORTED;
+  // the last code's place, in units of 16 bytes, fits 32 bits (64 GB a tensor)
+  if (c->page_stride > kMaxSpan || c->token_stride > kMaxSpan || c->head_stride > kMaxSpan ||
+      c->page_stride * (double)c->num_pages + c->token_stride * (double)c->page_size + c->head_stride * (double)c->heads >
+          (double)kMaxSpan)
     return FP8Q_ERR_UNSUPPORTED;
   // places of different tokens, heads or pages do not overlap
   if ((c->heads > 1 && c->head_stride < c->head_dim) || (c->page_size > 1 && c->token_stride < c->head_dim) ||

@@ -33,6 +33,7 @@ BAD_CACHES = [
     (dict(head_dim=0), 1), (dict(head_dim=72), 1), (dict(head_dim=24), 1), (dict(page_stride=2056), 1),
     (dict(token_stride=136), 1), (dict(head_stride=72), 1), (dict(head_dim=272, head_stride=272, token_stride=544), 2),
     (dict(num_pages=1 << 28), 2), (dict(page_size=1 << 31), 2), (dict(heads=1 << 20), 2),
+    (dict(page_stride=1 << 35), 2), (dict(page_stride=1 << 62), 2),
     (dict(head_stride=48), 1), (dict(head_stride=0), 1), (dict(token_stride=0), 1), (dict(page_stride=-2048), 1),
     (dict(k_codes=None), 1), (dict(v_codes=None), 1), (dict(k_codes=MIS), 1), (dict(k_scales=None), 1),
     (dict(v_scales=MIS4), 1),
