@@ -13,15 +13,16 @@
 // is off by 0.06 at position 10^6).  sincospi of the signed fraction follows; each block computes
 // the pairs of its tokens once, for all heads, into shared memory.
 //
-// A row (one head of one token) belongs to head_dim / 8 threads of a warp, padded to a power of
-// two; each holds two runs of 4 elements, chosen so that both elements of a rotated pair are its
-// own (halves layout: the runs at 4 i of either half; neighbours: 8 adjacent elements).  No
-// exchange is needed but the sums over the row, and q may be rotated in place.  A thread's elements
-// lie in four fp32 pairs, first elements of rotated pairs beside first ones, so that norm, rotation
-// and quotient take one instruction a pair.
+// A row (one head of one token) is cut into chunks of 8 elements, two to a thread (LPR threads a
+// row, a power of two): chunk c is two runs of 4 elements, chosen so that both elements of a
+// rotated pair are in it (halves layout: the runs at 4 c of either half; neighbours: 8 adjacent
+// elements).  No exchange is needed but the sums over the row, and q may be rotated in place.
+// A chunk lies in four fp32 pairs, first elements of rotated pairs beside first ones, so that norm,
+// rotation and quotient take one instruction a pair.
 //
-// A warp keeps its heads over the tokens of its block: what it does (q, k or v), its weights and
-// scales are settled once, and the rows of kBatch tokens are loaded together.
+// A block takes up to kTokens tokens and works out their angles and places first.  A warp then goes
+// through the tokens with its heads (32 / LPR rows at a time): what it does (q, k or v) is settled
+// once, its places move by a stride, and the loads of two tokens run ahead.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,10 +36,10 @@
 namespace fp8q {
 namespace append {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxWarps = 8;
+constexpr int kSmWarps = 24;                // an SM holds this many at 80 registers a thread
 constexpr int kMaxPairs = 128;              // rotated pairs of a row (head_dim <= 256)
-constexpr int kBatch = 4;                   // tokens of a block where there are many
+constexpr int kTokens = 16;                 // tokens of a block
 
 struct Params {
   KvPages c;
@@ -55,20 +56,21 @@ struct Params {
   int64_t q_out_stride;
   int tokens, q_heads;
   int q_units, kv_units;                    // warp steps for the q rows, the k rows (and the v rows)
+  int block_tokens;
   uint32_t* err;
 };
 
-// A thread's eight elements: a[0] holds the first elements of its rotated pairs 0, 1, a[1] of 2, 3;
+// A chunk of eight elements: a[0] holds the first elements of its rotated pairs 0, 1, a[1] of 2, 3;
 // b the second ones.  Where nothing is rotated the same places hold the elements in that order.
-struct Row {
+struct Chunk {
   float2 a[2], b[2];
 };
 
 // NEXT: pairs are neighbours (r0, r1 are 8 adjacent elements), else r0 holds first elements and r1
 // second ones
 template <bool NEXT>
-__device__ __forceinline__ Row unpack(uint2 r0, uint2 r1) {
-  Row y;
+__device__ __forceinline__ Chunk unpack(uint2 r0, uint2 r1) {
+  Chunk y;
   if constexpr (NEXT) {
     y.a[0] = make_float2(bf16_lo(r0.x), bf16_lo(r0.y));
     y.b[0] = make_float2(bf16_hi(r0.x), bf16_hi(r0.y));
@@ -83,7 +85,7 @@ __device__ __forceinline__ Row unpack(uint2 r0, uint2 r1) {
   return y;
 }
 template <bool NEXT>
-__device__ __forceinline__ void pack_bf16(const Row& y, uint2& r0, uint2& r1) {
+__device__ __forceinline__ void pack_bf16(const Chunk& y, uint2& r0, uint2& r1) {
   if constexpr (NEXT) {
     r0 = make_uint2(f32x2_to_bf16x2(y.a[0].x, y.b[0].x), f32x2_to_bf16x2(y.a[0].y, y.b[0].y));
     r1 = make_uint2(f32x2_to_bf16x2(y.a[1].x, y.b[1].x), f32x2_to_bf16x2(y.a[1].y, y.b[1].y));
@@ -93,7 +95,7 @@ __device__ __forceinline__ void pack_bf16(const Row& y, uint2& r0, uint2& r1) {
   }
 }
 template <int FMT, bool NEXT>
-__device__ __forceinline__ uint2 pack_codes(const Row& y) {
+__device__ __forceinline__ uint2 pack_codes(const Chunk& y) {
   if constexpr (NEXT) {
     return make_uint2(__byte_perm(cvt2<FMT>(y.a[0].x, y.b[0].x), cvt2<FMT>(y.a[0].y, y.b[0].y), 0x5410),
                       __byte_perm(cvt2<FMT>(y.a[1].x, y.b[1].x), cvt2<FMT>(y.a[1].y, y.b[1].y), 0x5410));
@@ -109,7 +111,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 // largest magnitude of the eight; any NaN gives NaN
-__device__ __forceinline__ float top_of(const Row& y) {
+__device__ __forceinline__ float top_of(const Chunk& y) {
   const float m0 = max_nan(fabsf(y.a[0].x), fabsf(y.a[0].y)), m1 = max_nan(fabsf(y.a[1].x), fabsf(y.a[1].y));
   const float m2 = max_nan(fabsf(y.b[0].x), fabsf(y.b[0].y)), m3 = max_nan(fabsf(y.b[1].x), fabsf(y.b[1].y));
   return max_nan(max_nan(m0, m1), max_nan(m2, m3));
@@ -143,7 +145,7 @@ __device__ __forceinline__ float quotient(float x, float d, float r) {
 // that saturates, or far below the smallest code).  0 gives signed zeros, infinity zeros but NaN
 // for an infinite element, NaN gives NaN.
 template <int FMT, bool NEXT>
-__device__ __forceinline__ uint2 codes_any(Row y, float d) {
+__device__ __forceinline__ uint2 codes_any(Chunk y, float d) {
   const float m = fabsf(d);
   const bool zero = d == 0.0f, inf = m == __int_as_float(0x7F800000);
   const float by = m < 0x1.0p-60f ? 0x1.0p100f : m > 0x1.0p100f ? 0x1.0p-20f : 1.0f;
@@ -162,18 +164,18 @@ __device__ __forceinline__ uint2 codes_any(Row y, float d) {
   return pack_codes<FMT, NEXT>(y);
 }
 
-// Codes of y / d.  GIVEN: the quotients may overflow (a scale that does not come from the row)
-template <int FMT, bool NEXT, bool GIVEN>
-__device__ __forceinline__ uint2 codes_of(const Row& y, const Divisor& v) {
+// Codes of y / d
+template <int FMT, bool NEXT>
+__device__ __forceinline__ uint2 codes_of(const Chunk& y, const Divisor& v) {
   // quant4_fast's three steps on negated pairs: p = -q0, f = the residual, n = -q
   const float2 d2 = make_float2(v.d, v.d), nr = make_float2(-v.r, -v.r);
-  Row p, n;
+  Chunk p, n;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     p.a[i] = __fmul2_rn(y.a[i], nr);
     p.b[i] = __fmul2_rn(y.b[i], nr);
   }
-  if (!v.fast || (GIVEN && !(top_of(p) < 0x1.0p100f))) return codes_any<FMT, NEXT>(y, v.d);
+  if (!v.fast || !(top_of(p) < 0x1.0p100f)) return codes_any<FMT, NEXT>(y, v.d);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     n.a[i] = __ffma2_rn(__ffma2_rn(p.a[i], d2, y.a[i]), nr, p.a[i]);
@@ -190,154 +192,196 @@ __device__ __forceinline__ uint2 load8(const void* p) {
   return v;
 }
 
-template <int FMT, int LPR, bool NEXT, int BT>
-__global__ void __launch_bounds__(kThreads, 4) k_append(const Params p) {
-  __shared__ __align__(16) float cosine[BT][kMaxPairs], sine[BT][kMaxPairs];
-  constexpr int RPW = 32 / LPR;             // rows a warp takes at once
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int li = lane % LPR, sub = lane / LPR;
-  const int D = p.c.head_dim;
-  const bool inside = 8 * li < D;
-  const bool rotated = 8 * li < p.rot;
-  const bool split = rotated && !NEXT;
-  const int o0 = split ? 4 * li : 8 * li, o1 = split ? p.rot / 2 + 4 * li : 8 * li + 4;
+template <int LPR>
+struct Shared {
+  float cosine[kTokens][kMaxPairs], sine[kTokens][kMaxPairs];
+  float weights[2][8 * 2 * LPR];            // of q and k, chunk after chunk
+  int2 slots[kTokens];                      // slot (-1: not at all) and its place in units of 16 bytes
+};
 
-  allow_dependent_launch();
-  grid_dependency_wait();
-
-  const int t0 = blockIdx.x * BT;
-  const int nt = min(BT, p.tokens - t0);
-  if (p.rot > 0) {
-    const int pairs = p.rot / 2;
-    for (int i = threadIdx.x; i < BT * kMaxPairs; i += kThreads) {
-      const int tk = i / kMaxPairs, f = i % kMaxPairs;
-      if (tk < nt && f < pairs) {
-        const unsigned long long a = (unsigned long long)(long long)__ldg(p.positions + t0 + tk) * __ldg(p.turns + f);
-        float sn, cs;
-        sincospif((float)(int)(a >> 32) * 0x1.0p-31f, &sn, &cs);
-        cosine[tk][f] = cs * p.gain;
-        sine[tk][f] = sn * p.gain;
-      }
-    }
-    __syncthreads();
+// Rows u * 32 / LPR .. of one kind (0 q, 1 k, 2 v) of tokens t0 .. t0 + nt - 1.  FULL: rows of 16 LPR
+// elements, all of them or none rotated (none: NEXT), so a thread's runs lie at fixed distances
+template <int FMT, int LPR, bool NEXT, bool FULL, int KIND>
+__device__ __forceinline__ void rows(const Params& p, const Shared<LPR>& sh, int u, int t0, int nt) {
+  const int lane = threadIdx.x & 31;
+  const int li = lane % LPR, head = u * (32 / LPR) + lane / LPR;
+  const int D = FULL ? 16 * LPR : p.c.head_dim;
+  const bool own = head < (KIND == 0 ? p.q_heads : p.c.heads);
+  bool live[2], rotated[2];
+  int o0[2], o1[2];                         // a chunk's runs
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int at = li + c * LPR;
+    live[c] = own && (FULL || 8 * at < D);
+    rotated[c] = FULL ? p.rot > 0 : 8 * at < p.rot;
+    const bool split = FULL ? !NEXT : rotated[c] && !NEXT;
+    o0[c] = split ? 4 * at : 8 * at;
+    o1[c] = split ? (FULL ? 8 * LPR : p.rot / 2) + 4 * at : 8 * at + 4;
   }
-
-  const int units = p.q_units + 2 * p.kv_units;
+  const int64_t stride = KIND == 0 ? p.q_stride : KIND == 1 ? p.k_stride : p.v_stride;
+  const uint16_t* src = (KIND == 0 ? p.q : KIND == 1 ? p.k : p.v) + t0 * stride + (int64_t)head * D + o0[0];
+  uint16_t* dst = KIND == 0 ? p.q_out + t0 * p.q_out_stride + (int64_t)head * D + o0[0] : nullptr;
+  uint8_t* const codes_at = KIND == 0 ? nullptr : (KIND == 1 ? p.c.k : p.c.v) + (int64_t)head * p.c.head_stride + o0[0];
   const int64_t cache_slots = (int64_t)p.c.num_pages * p.c.page_size;
-  for (int unit = blockIdx.y * kWarps + warp; unit < units; unit += gridDim.y * kWarps) {
-    int u = unit, kind = 0;                 // 0 q, 1 k, 2 v
-    if (u >= p.q_units) {
-      u -= p.q_units;
-      kind = 1;
-      if (u >= p.kv_units) {
-        u -= p.kv_units;
-        kind = 2;
-      }
-    }
-    const int head = u * RPW + sub;
-    const bool live = inside && head < (kind == 0 ? p.q_heads : p.c.heads);
-    const int64_t stride = kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride;
-    const uint16_t* src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + t0 * stride + (int64_t)head * D;
-    const uint16_t* weight = kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr;
-    uint2 r0[BT], r1[BT];
-    int64_t slot[BT];
-#pragma unroll
-    for (int j = 0; j < BT; ++j) {
-      r0[j] = r1[j] = make_uint2(0, 0);
-      slot[j] = -1;
-      if (j < nt) {
-        if (live) {
-          r0[j] = load8(src + j * stride + o0);
-          r1[j] = load8(src + j * stride + o1);
-        }
-        if (kind != 0) slot[j] = __ldg(p.slots + t0 + j);
-      }
-    }
-    Row w;
-    if (weight) {
-      uint2 w0 = make_uint2(0, 0), w1 = w0;
-      if (inside) {
-        w0 = __ldg(reinterpret_cast<const uint2*>(weight + o0));
-        w1 = __ldg(reinterpret_cast<const uint2*>(weight + o1));
-      }
-      w = unpack<NEXT>(w0, w1);
-    }
-    float* scales = kind == 1 ? p.c.ks : p.c.vs;
-    Divisor by;
-    by.d = by.r = 1.0f;
-    by.fast = true;
-    if (kind != 0 && p.c.gran != 3 && live) by = divisor_of(__ldg(scales + (p.c.gran == 0 ? 0 : head)));
+  float* const scales = (KIND == 1 ? p.c.ks : p.c.vs) + (p.c.gran == 3 ? head * cache_slots : 0);
+  const bool norm = KIND != 2 && (KIND == 0 ? p.q_weight : p.k_weight) != nullptr;
+  Divisor by;
+  by.d = by.r = 1.0f;
+  by.fast = true;
+  if (KIND != 0 && p.c.gran != 3 && own) by = divisor_of(__ldg(scales + (p.c.gran == 0 ? 0 : head)));
 
+  struct Raw {
+    uint2 r[2][2];
+  };
+  auto load = [&](Raw& x) {
 #pragma unroll
-    for (int j = 0; j < BT; ++j) {
-      if (j >= nt) break;
-      if (kind != 0) {
-        if (slot[j] < 0) continue;          // a padded row; the same for the whole warp
-        if (slot[j] >= cache_slots) {
-          raise_device_error(p.err, kErrBadPage);
-          continue;
-        }
+    for (int c = 0; c < 2; ++c)
+      if (live[c]) {
+        x.r[c][0] = load8(src + (o0[c] - o0[0]));
+        x.r[c][1] = load8(src + (o1[c] - o0[0]));
       }
-      Row y = unpack<NEXT>(r0[j], r1[j]);
-      if (weight) {
-        float2 ss = __fmul2_rn(y.a[0], y.a[0]);
-        ss = __ffma2_rn(y.a[1], y.a[1], ss);
-        ss = __ffma2_rn(y.b[0], y.b[0], ss);
-        ss = __ffma2_rn(y.b[1], y.b[1], ss);
-        float sum = ss.x + ss.y;
+    src += stride;
+  };
+  // row j of the block's tokens, and the load of row j + 2 into its place
+  auto row = [&](Raw& x, int j) {
+    Chunk y[2] = {unpack<NEXT>(x.r[0][0], x.r[0][1]), unpack<NEXT>(x.r[1][0], x.r[1][1])};
+    if (j + 2 < nt) load(x);
+    if (norm) {
+      float2 ss = __fmul2_rn(y[0].a[0], y[0].a[0]);
+      ss = __ffma2_rn(y[0].a[1], y[0].a[1], ss);
+      ss = __ffma2_rn(y[0].b[0], y[0].b[0], ss);
+      ss = __ffma2_rn(y[0].b[1], y[0].b[1], ss);
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const float f = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
-        const float2 f2 = make_float2(f, f);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          y.a[i] = __fmul2_rn(__fmul2_rn(y.a[i], f2), w.a[i]);
-          y.b[i] = __fmul2_rn(__fmul2_rn(y.b[i], f2), w.b[i]);
-        }
+      for (int i = 0; i < 2; ++i) {
+        ss = __ffma2_rn(y[1].a[i], y[1].a[i], ss);
+        ss = __ffma2_rn(y[1].b[i], y[1].b[i], ss);
       }
-      if (kind != 2 && rotated) {
-        const float4 cs = *reinterpret_cast<const float4*>(&cosine[j][4 * li]);
-        const float4 sn = *reinterpret_cast<const float4*>(&sine[j][4 * li]);
-        const float2 c[2] = {make_float2(cs.x, cs.y), make_float2(cs.z, cs.w)};
-        const float2 s[2] = {make_float2(sn.x, sn.y), make_float2(sn.z, sn.w)};
+      float sum = ss.x + ss.y;
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      const float f = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
+      const float2 f2 = make_float2(f, f);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float4* w = reinterpret_cast<const float4*>(&sh.weights[KIND & 1][8 * (li + c * LPR)]);
+        const float4 wa = w[0], wb = w[1];
+        y[c].a[0] = __fmul2_rn(__fmul2_rn(y[c].a[0], f2), make_float2(wa.x, wa.y));
+        y[c].a[1] = __fmul2_rn(__fmul2_rn(y[c].a[1], f2), make_float2(wa.z, wa.w));
+        y[c].b[0] = __fmul2_rn(__fmul2_rn(y[c].b[0], f2), make_float2(wb.x, wb.y));
+        y[c].b[1] = __fmul2_rn(__fmul2_rn(y[c].b[1], f2), make_float2(wb.z, wb.w));
+      }
+    }
+    if (KIND != 2) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (!rotated[c]) continue;
+        const float4 cs = *reinterpret_cast<const float4*>(&sh.cosine[j][4 * (li + c * LPR)]);
+        const float4 sn = *reinterpret_cast<const float4*>(&sh.sine[j][4 * (li + c * LPR)]);
+        const float2 cc[2] = {make_float2(cs.x, cs.y), make_float2(cs.z, cs.w)};
+        const float2 sc[2] = {make_float2(sn.x, sn.y), make_float2(sn.z, sn.w)};
         const float2 minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 a = y.a[i], b = y.b[i];
-          y.a[i] = __ffma2_rn(a, c[i], __fmul2_rn(b, __fmul2_rn(s[i], minus)));
-          y.b[i] = __ffma2_rn(b, c[i], __fmul2_rn(a, s[i]));
+          const float2 a = y[c].a[i], b = y[c].b[i];
+          y[c].a[i] = __ffma2_rn(a, cc[i], __fmul2_rn(b, __fmul2_rn(sc[i], minus)));
+          y[c].b[i] = __ffma2_rn(b, cc[i], __fmul2_rn(a, sc[i]));
         }
       }
-      if (kind == 0) {
-        if (live) {
-          uint16_t* dst = p.q_out + (t0 + j) * p.q_out_stride + (int64_t)head * D;
-          uint2 x0, x1;
-          pack_bf16<NEXT>(y, x0, x1);
-          *reinterpret_cast<uint2*>(dst + o0) = x0;
-          *reinterpret_cast<uint2*>(dst + o1) = x1;
+    }
+    if constexpr (KIND == 0) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint2 x0, x1;
+        pack_bf16<NEXT>(y[c], x0, x1);
+        if (live[c]) {
+          *reinterpret_cast<uint2*>(dst + (o0[c] - o0[0])) = x0;
+          *reinterpret_cast<uint2*>(dst + (o1[c] - o0[0])) = x1;
         }
-        continue;
       }
-      uint2 codes;
+      dst += p.q_out_stride;
+    } else {
+      const int2 to = sh.slots[j];
+      if (to.x < 0) return;                 // the same for the whole block
+      Divisor d = by;
       if (p.c.gran == 3) {
-        float top = top_of(y);
+        float top = max_nan(top_of(y[0]), top_of(y[1]));
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         const GroupScale g = make_group_scale<FMT>(top);
-        if (live && li == 0) scales[(int64_t)head * cache_slots + slot[j]] = g.s;
-        codes = codes_of<FMT, NEXT, false>(y, Divisor{g.d, g.r, g.fast});
-      } else {
-        codes = codes_of<FMT, NEXT, true>(y, by);
+        if (own && li == 0) scales[to.x] = g.s;
+        d = Divisor{g.d, g.r, g.fast};
       }
-      if (live) {
-        const uint32_t page = div_u32((uint32_t)slot[j], p.c.page_div);
-        const uint32_t off = (uint32_t)slot[j] - page * (uint32_t)p.c.page_size;
-        uint8_t* dst = (kind == 1 ? p.c.k : p.c.v) + (int64_t)page * p.c.page_stride + (int64_t)off * p.c.token_stride +
-                       (int64_t)head * p.c.head_stride;
-        *reinterpret_cast<uint32_t*>(dst + o0) = codes.x;
-        *reinterpret_cast<uint32_t*>(dst + o1) = codes.y;
+      uint8_t* at = codes_at + (uint64_t)(uint32_t)to.y * 16;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint2 codes = codes_of<FMT, NEXT>(y[c], d);
+        if (live[c]) {
+          *reinterpret_cast<uint32_t*>(at + (o0[c] - o0[0])) = codes.x;
+          *reinterpret_cast<uint32_t*>(at + (o1[c] - o0[0])) = codes.y;
+        }
       }
     }
+  };
+
+  Raw a, b;                                 // places past head_dim stay zero
+#pragma unroll
+  for (int c = 0; c < 2; ++c) a.r[c][0] = a.r[c][1] = b.r[c][0] = b.r[c][1] = make_uint2(0, 0);
+  load(a);
+  if (nt > 1) load(b);
+#pragma unroll 1
+  for (int j = 0; j < nt; j += 2) {
+    row(a, j);
+    if (j + 1 < nt) row(b, j + 1);
+  }
+}
+
+template <int FMT, int LPR, bool NEXT, bool FULL>
+__global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append(const Params p) {
+  __shared__ __align__(16) Shared<LPR> sh;
+  const int64_t cache_slots = (int64_t)p.c.num_pages * p.c.page_size;
+  const int warps = blockDim.x >> 5;
+  allow_dependent_launch();
+  grid_dependency_wait();
+
+  const int t0 = blockIdx.x * p.block_tokens;
+  const int nt = min(p.block_tokens, p.tokens - t0);
+  const int pairs = p.rot / 2;
+  for (int i = threadIdx.x; i < nt * kMaxPairs; i += blockDim.x) {
+    const int tk = i / kMaxPairs, f = i % kMaxPairs;
+    if (f >= pairs) continue;
+    const unsigned long long a = (unsigned long long)(long long)__ldg(p.positions + t0 + tk) * __ldg(p.turns + f);
+    float sn, cs;
+    sincospif((float)(int)(a >> 32) * 0x1.0p-31f, &sn, &cs);
+    sh.cosine[tk][f] = cs * p.gain;
+    sh.sine[tk][f] = sn * p.gain;
+  }
+  for (int i = threadIdx.x; i < 2 * 2 * LPR; i += blockDim.x) {
+    const int which = i / (2 * LPR), at = i % (2 * LPR);
+    const uint16_t* weight = which == 0 ? p.q_weight : p.k_weight;
+    if (weight && 8 * at < p.c.head_dim) {
+      const bool split = 8 * at < p.rot && !NEXT;
+      const Chunk w = unpack<NEXT>(__ldg(reinterpret_cast<const uint2*>(weight + (split ? 4 * at : 8 * at))),
+                                   __ldg(reinterpret_cast<const uint2*>(weight + (split ? pairs + 4 * at : 8 * at + 4))));
+      float4* to = reinterpret_cast<float4*>(&sh.weights[which][8 * at]);
+      to[0] = make_float4(w.a[0].x, w.a[0].y, w.a[1].x, w.a[1].y);
+      to[1] = make_float4(w.b[0].x, w.b[0].y, w.b[1].x, w.b[1].y);
+    }
+  }
+  if (threadIdx.x < nt) {
+    const int64_t slot = __ldg(p.slots + t0 + threadIdx.x);
+    if (slot >= cache_slots) raise_device_error(p.err, kErrBadPage);
+    const uint32_t page = div_u32((uint32_t)slot, p.c.page_div);
+    const uint32_t off = (uint32_t)slot - page * (uint32_t)p.c.page_size;
+    // the last code's place fits 32 bits (checked on the host)
+    sh.slots[threadIdx.x] = make_int2(slot >= 0 && slot < cache_slots ? (int)slot : -1,
+                                      (int)(page * (uint32_t)(p.c.page_stride >> 4) + off * (uint32_t)(p.c.token_stride >> 4)));
+  }
+  __syncthreads();
+  const int units = p.q_units + 2 * p.kv_units;
+  for (int u = blockIdx.y * warps + (threadIdx.x >> 5); u < units; u += gridDim.y * warps) {
+    if (u < p.q_units) rows<FMT, LPR, NEXT, FULL, 0>(p, sh, u, t0, nt);
+    else if (u < p.q_units + p.kv_units) rows<FMT, LPR, NEXT, FULL, 1>(p, sh, u - p.q_units, t0, nt);
+    else rows<FMT, LPR, NEXT, FULL, 2>(p, sh, u - p.q_units - p.kv_units, t0, nt);
   }
 }
 
@@ -348,20 +392,26 @@ cudaError_t launch(Params& p, cudaStream_t st) {
   p.kv_units = (p.c.heads + rpw - 1) / rpw;
   const int units = p.q_units + 2 * p.kv_units;
   const int64_t sms = std::max(1, device_sm_count());
-  // kBatch tokens a block once that leaves some waves of blocks, else one, and then as many blocks a
-  // token as the machine has room for
-  if (p.tokens >= sms * 4 * kBatch)
-    return launch_pdl(k_append<FMT, LPR, NEXT, kBatch>, dim3((p.tokens + kBatch - 1) / kBatch), dim3(kThreads), 0, st, p);
-  const int64_t most = (units + kWarps - 1) / kWarps, room = std::max<int64_t>(1, sms * 4 / p.tokens);
-  return launch_pdl(k_append<FMT, LPR, NEXT, 1>, dim3(p.tokens, (unsigned)std::min(most, room)), dim3(kThreads), 0, st, p);
+  // as many warps a block as leaves the fewest without a unit in the last turn
+  int warps = std::min(units, kMaxWarps);
+  for (int w = warps; w >= 4; --w)
+    if ((units + w - 1) / w * w < (units + warps - 1) / warps * warps) warps = w;
+  const int64_t room = sms * (kSmWarps / warps);
+  // tokens a block so that the blocks are one wave, or several of kTokens; where there are fewer tokens
+  // than blocks, several blocks a token
+  p.block_tokens = (int)std::min<int64_t>(kTokens, std::max<int64_t>(1, (p.tokens + room - 1) / room));
+  const unsigned x = (unsigned)((p.tokens + p.block_tokens - 1) / p.block_tokens);
+  const unsigned y = (unsigned)std::min<int64_t>((units + warps - 1) / warps, std::max<int64_t>(1, room / p.tokens));
+  const bool full = p.c.head_dim == 16 * LPR && (p.rot == p.c.head_dim || (NEXT && p.rot == 0));
+  return launch_pdl(full ? k_append<FMT, LPR, NEXT, true> : k_append<FMT, LPR, NEXT, false>, dim3(x, y), dim3(32 * warps), 0,
+                    st, p);
 }
 
-template <int FMT, bool NEXT>
-cudaError_t launch_lanes(Params& p, cudaStream_t st) {
-  if (p.c.head_dim <= 32) return launch<FMT, 4, NEXT>(p, st);
-  if (p.c.head_dim <= 64) return launch<FMT, 8, NEXT>(p, st);
-  if (p.c.head_dim <= 128) return launch<FMT, 16, NEXT>(p, st);
-  return launch<FMT, 32, NEXT>(p, st);
+template <int FMT>
+cudaError_t launch_lanes(Params& p, bool next, cudaStream_t st) {
+  if (p.c.head_dim <= 64) return next ? launch<FMT, 4, true>(p, st) : launch<FMT, 4, false>(p, st);
+  if (p.c.head_dim <= 128) return next ? launch<FMT, 8, true>(p, st) : launch<FMT, 8, false>(p, st);
+  return next ? launch<FMT, 16, true>(p, st) : launch<FMT, 16, false>(p, st);
 }
 
 }  // namespace append
@@ -390,9 +440,8 @@ cudaError_t launch_kv_append(const KvPages& c, int fmt, const KvAppend& a, cudaS
   p.tokens = (int)a.tokens;
   p.q_heads = a.q_heads;
   p.err = device_error_word();
-  if (fmt == kE4M3)
-    return a.interleaved ? append::launch_lanes<kE4M3, true>(p, st) : append::launch_lanes<kE4M3, false>(p, st);
-  return a.interleaved ? append::launch_lanes<kE5M2, true>(p, st) : append::launch_lanes<kE5M2, false>(p, st);
+  const bool next = a.interleaved || a.rot == 0;
+  return fmt == kE4M3 ? append::launch_lanes<kE4M3>(p, next, st) : append::launch_lanes<kE5M2>(p, next, st);
 }
 
 }  // namespace fp8q
