@@ -195,14 +195,14 @@ __device__ __forceinline__ uint2 load8(const void* p) {
 template <int LPR>
 struct Shared {
   float cosine[kTokens][kMaxPairs], sine[kTokens][kMaxPairs];
-  float weights[2][8 * 2 * LPR];            // of q and k, chunk after chunk
+  float weights[2][2][4 * 2 * LPR];         // of q and k: the chunks' first runs, their second ones
   int2 slots[kTokens];                      // slot (-1: not at all) and its place in units of 16 bytes
 };
 
 // Rows u * 32 / LPR .. of one kind (0 q, 1 k, 2 v) of tokens t0 .. t0 + nt - 1.  FULL: rows of 16 LPR
 // elements, all of them or none rotated (none: NEXT), so a thread's runs lie at fixed distances
 template <int FMT, int LPR, bool NEXT, bool FULL, int KIND>
-__device__ __forceinline__ void rows(const Params& p, const Shared<LPR>& sh, int u, int t0, int nt) {
+__device__ __forceinline__ void rows(const Params& p, const Shared<LPR>& sh, int u, int t0, int nt, bool first) {
   const int lane = threadIdx.x & 31;
   const int li = lane % LPR, head = u * (32 / LPR) + lane / LPR;
   const int D = FULL ? 16 * LPR : p.c.head_dim;
@@ -263,8 +263,8 @@ __device__ __forceinline__ void rows(const Params& p, const Shared<LPR>& sh, int
       const float2 f2 = make_float2(f, f);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float4* w = reinterpret_cast<const float4*>(&sh.weights[KIND & 1][8 * (li + c * LPR)]);
-        const float4 wa = w[0], wb = w[1];
+        const float4 wa = *reinterpret_cast<const float4*>(&sh.weights[KIND & 1][0][4 * (li + c * LPR)]);
+        const float4 wb = *reinterpret_cast<const float4*>(&sh.weights[KIND & 1][1][4 * (li + c * LPR)]);
         y[c].a[0] = __fmul2_rn(__fmul2_rn(y[c].a[0], f2), make_float2(wa.x, wa.y));
         y[c].a[1] = __fmul2_rn(__fmul2_rn(y[c].a[1], f2), make_float2(wa.z, wa.w));
         y[c].b[0] = __fmul2_rn(__fmul2_rn(y[c].b[0], f2), make_float2(wb.x, wb.y));
@@ -328,6 +328,7 @@ __device__ __forceinline__ void rows(const Params& p, const Shared<LPR>& sh, int
   for (int c = 0; c < 2; ++c) a.r[c][0] = a.r[c][1] = b.r[c][0] = b.r[c][1] = make_uint2(0, 0);
   load(a);
   if (nt > 1) load(b);
+  if (first) __syncthreads();               // the shared part is complete; every warp passes this once
 #pragma unroll 1
   for (int j = 0; j < nt; j += 2) {
     row(a, j);
@@ -345,6 +346,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append
 
   const int t0 = blockIdx.x * p.block_tokens;
   const int nt = min(p.block_tokens, p.tokens - t0);
+  const int units = p.q_units + 2 * p.kv_units;
+  int u = blockIdx.y * warps + (threadIdx.x >> 5);
   const int pairs = p.rot / 2;
   for (int i = threadIdx.x; i < nt * kMaxPairs; i += blockDim.x) {
     const int tk = i / kMaxPairs, f = i % kMaxPairs;
@@ -362,9 +365,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append
       const bool split = 8 * at < p.rot && !NEXT;
       const Chunk w = unpack<NEXT>(__ldg(reinterpret_cast<const uint2*>(weight + (split ? 4 * at : 8 * at))),
                                    __ldg(reinterpret_cast<const uint2*>(weight + (split ? pairs + 4 * at : 8 * at + 4))));
-      float4* to = reinterpret_cast<float4*>(&sh.weights[which][8 * at]);
-      to[0] = make_float4(w.a[0].x, w.a[0].y, w.a[1].x, w.a[1].y);
-      to[1] = make_float4(w.b[0].x, w.b[0].y, w.b[1].x, w.b[1].y);
+      *reinterpret_cast<float4*>(&sh.weights[which][0][4 * at]) = make_float4(w.a[0].x, w.a[0].y, w.a[1].x, w.a[1].y);
+      *reinterpret_cast<float4*>(&sh.weights[which][1][4 * at]) = make_float4(w.b[0].x, w.b[0].y, w.b[1].x, w.b[1].y);
     }
   }
   if (threadIdx.x < nt) {
@@ -376,12 +378,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append
     sh.slots[threadIdx.x] = make_int2(slot >= 0 && slot < cache_slots ? (int)slot : -1,
                                       (int)(page * (uint32_t)(p.c.page_stride >> 4) + off * (uint32_t)(p.c.token_stride >> 4)));
   }
-  __syncthreads();
-  const int units = p.q_units + 2 * p.kv_units;
-  for (int u = blockIdx.y * warps + (threadIdx.x >> 5); u < units; u += gridDim.y * warps) {
-    if (u < p.q_units) rows<FMT, LPR, NEXT, FULL, 0>(p, sh, u, t0, nt);
-    else if (u < p.q_units + p.kv_units) rows<FMT, LPR, NEXT, FULL, 1>(p, sh, u - p.q_units, t0, nt);
-    else rows<FMT, LPR, NEXT, FULL, 2>(p, sh, u - p.q_units - p.kv_units, t0, nt);
+  if (u >= units) __syncthreads();
+  for (bool first = true; u < units; u += gridDim.y * warps, first = false) {
+    if (u < p.q_units) rows<FMT, LPR, NEXT, FULL, 0>(p, sh, u, t0, nt, first);
+    else if (u < p.q_units + p.kv_units) rows<FMT, LPR, NEXT, FULL, 1>(p, sh, u - p.q_units, t0, nt, first);
+    else rows<FMT, LPR, NEXT, FULL, 2>(p, sh, u - p.q_units - p.kv_units, t0, nt, first);
   }
 }
 
@@ -397,9 +398,10 @@ cudaError_t launch(Params& p, cudaStream_t st) {
   for (int w = warps; w >= 4; --w)
     if ((units + w - 1) / w * w < (units + warps - 1) / warps * warps) warps = w;
   const int64_t room = sms * (kSmWarps / warps);
-  // tokens a block so that the blocks are one wave, or several of kTokens; where there are fewer tokens
-  // than blocks, several blocks a token
-  p.block_tokens = (int)std::min<int64_t>(kTokens, std::max<int64_t>(1, (p.tokens + room - 1) / room));
+  // tokens a block so that the blocks fill whole waves; where there are fewer tokens than blocks of a
+  // wave, several blocks a token
+  const int64_t waves = (p.tokens + room * kTokens - 1) / (room * kTokens);
+  p.block_tokens = (int)((p.tokens + room * waves - 1) / (room * waves));
   const unsigned x = (unsigned)((p.tokens + p.block_tokens - 1) / p.block_tokens);
   const unsigned y = (unsigned)std::min<int64_t>((units + warps - 1) / warps, std::max<int64_t>(1, room / p.tokens));
   const bool full = p.c.head_dim == 16 * LPR && (p.rot == p.c.head_dim || (NEXT && p.rot == 0));
