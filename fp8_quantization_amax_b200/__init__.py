@@ -749,35 +749,26 @@ def fp8_dequantize_mx(codes: torch.Tensor, scales: torch.Tensor, fmt: int = E4M3
 
 # ------------------------------------------------------------------ paged KV cache
 
-def _paged_on(dev: int, *tensors) -> None:
-    """Every given tensor lies on CUDA device `dev`."""
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors of a call must be on one CUDA device (this library has no CPU path)")
+_calls = None
 
 
-def _expect(t, name: str, dtype, shape=None) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _call_on(dev: int, fn: str, *args) -> None:
-    """Call the library with `dev` current, on its current stream (the last argument)."""
-    if torch.cuda.current_device() == dev:
-        _check(fn, getattr(lib(), fn)(*args, _raw_stream_of(dev)))
-    else:
-        with torch.cuda.device(dev):
-            _check(fn, getattr(lib(), fn)(*args, _raw_stream_of(dev)))
-
-
-def _raw_stream_of(dev: int) -> int:
-    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+def _load_calls():
+    """The module _torch_calls (csrc/torch_calls.cpp), bound to the library's entry points.  A decoding
+    step makes these calls for every layer: their checks run there and not in Python."""
+    global _calls
+    L = lib()
+    with _lock:
+        if _calls is None:
+            try:
+                from . import _torch_calls
+            except ImportError as e:
+                raise ImportError("_torch_calls.so is missing or does not load; build it with "
+                                  "`python -m fp8_quantization_amax_b200.build`") from e
+            _torch_calls.bind(*[ctypes.cast(getattr(L, fn), ctypes.c_void_p).value
+                                for fn in ("fp8_attention_paged", "fp8q_attention_workspace_bytes", "fp8_kv_append",
+                                           "fp8_kv_pages_update", "fp8q_pages_workspace_bytes")], Fp8qError, torch.OutOfMemoryError)
+            _calls = _torch_calls
+    return _calls
 
 
 def kv_page_scale_shape(num_pages: int, page_size: int, heads: int, gran: int) -> tuple:
@@ -785,40 +776,6 @@ def kv_page_scale_shape(num_pages: int, page_size: int, heads: int, gran: int) -
     if gran == KV_PER_TOKEN:
         return (heads, num_pages * page_size)
     return kv_scale_shape(num_pages * page_size, heads, gran)
-
-
-def _pages_struct(k_cache, v_cache, k_scales, v_scales, fmt: int, gran: int) -> _KvPages:
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != torch.uint8:
-            raise TypeError(f"{name} must be torch.uint8, got {t.dtype}")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must both be [num_pages][page_size][heads][head_dim] with equal strides")
-    n, size, heads, d = k_cache.shape
-    page, token, head, one = k_cache.stride()
-    if one != 1:
-        raise ValueError("k_cache and v_cache must be contiguous along head_dim")
-    shape = kv_page_scale_shape(n, size, heads, gran)
-    _expect(k_scales, "k_scales", torch.float32, shape)
-    _expect(v_scales, "v_scales", torch.float32, shape)
-    # strides of single-entry dimensions are not used
-    return _KvPages(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), n, size, heads, d,
-                    page if n > 1 else 0, token if size > 1 else 0, head if heads > 1 else 0, fmt, gran)
-
-
-def _heads_of(x: torch.Tensor, name: str) -> int:
-    """Token stride of bf16 [tokens][heads][head_dim] whose heads are contiguous within a token."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be 3-D [tokens][heads][head_dim]")
-    token, head, one = x.stride()
-    if (one != 1 and x.shape[2] > 1) or (head != x.shape[2] and x.shape[1] > 1):
-        raise ValueError(f"{name} must be contiguous within a token")
-    return token if x.shape[0] > 1 else x.shape[1] * x.shape[2]
 
 
 def pages_workspace_bytes(batch: int, max_tokens: int) -> int:
@@ -837,47 +794,8 @@ def fp8_kv_pages_update(block_table: torch.Tensor, lens: torch.Tensor, added: to
     negative for one that ends.  -> (slots int64 [max_tokens], positions int32 [max_tokens], offsets
     int32 [batch + 1], served int32 [batch], lens_out, free_count_out); max_tokens, an upper bound of
     the added tokens known on the host, may be left out when slots is given."""
-    i32 = torch.int32
-    _expect(block_table, "block_table", i32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be 2-D [batch][max_pages]")
-    batch, max_pages = block_table.shape
-    _expect(lens, "lens", i32, (batch,))
-    _expect(added, "added", i32, (batch,))
-    _expect(free_pages, "free_pages", i32)
-    _expect(free_count, "free_count", i32, (1,))
-    if max_tokens is None:
-        if slots is None:
-            raise ValueError("max_tokens or slots must be given")
-        max_tokens = slots.numel()
-    dev = block_table.get_device()
-    if slots is None:
-        slots = torch.empty(max_tokens, dtype=torch.int64, device=block_table.device)
-    if positions is None:
-        positions = torch.empty(max_tokens, dtype=i32, device=block_table.device)
-    if offsets is None:
-        offsets = torch.empty(batch + 1, dtype=i32, device=block_table.device)
-    if served is None:
-        served = torch.empty(batch, dtype=i32, device=block_table.device)
-    lens_out = lens if lens_out is None else lens_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    _expect(slots, "slots", torch.int64, (max_tokens,))
-    _expect(positions, "positions", i32, (max_tokens,))
-    _expect(offsets, "offsets", i32, (batch + 1,))
-    _expect(served, "served", i32, (batch,))
-    _expect(lens_out, "lens_out", i32, (batch,))
-    _expect(free_count_out, "free_count_out", i32, (1,))
-    _paged_on(dev, block_table, lens, added, free_pages, free_count, slots, positions, offsets, served, lens_out,
-              free_count_out, ws)
-    if dev < 0:
-        raise ValueError("block_table must be a CUDA tensor (this library has no CPU path)")
-    ws = _workspace(pages_workspace_bytes(batch, max_tokens), block_table.device, ws)
-    _call_on(dev, "fp8_kv_pages_update", block_table.data_ptr(), batch, max_pages, page_size, lens.data_ptr(),
-             added.data_ptr(), lens_out.data_ptr(), free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(),
-             free_count_out.data_ptr(), max_tokens, slots.data_ptr(), positions.data_ptr(), offsets.data_ptr(),
-             served.data_ptr(), None if ws is None else ws.data_ptr(),
-             0 if ws is None else ws.numel() * ws.element_size())
-    return slots, positions, offsets, served, lens_out, free_count_out
+    return (_calls or _load_calls()).update(block_table, lens, added, free_pages, free_count, page_size, max_tokens, slots,
+                                            positions, offsets, served, lens_out, free_count_out, ws)
 
 
 def rope_turns(rot_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -902,49 +820,10 @@ def fp8_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slot
     slots (int64 [tokens], negative: padding); -> q_out, bf16 [tokens][q_heads][head_dim] (may be q).
     q, k, v: bf16 [tokens][heads][head_dim], contiguous within a token.  KV_PER_TENSOR and KV_PER_HEAD
     read the scales, KV_PER_TOKEN writes them."""
-    ks, vs = _heads_of(k, "k"), _heads_of(v, "v")
-    cache = _pages_struct(k_cache, v_cache, k_scales, v_scales, fmt, gran)
-    tokens, heads, d = k.shape
-    if v.shape != k.shape or heads != cache.heads or d != cache.head_dim:
-        raise ValueError("k and v must both be [tokens][heads][head_dim] of the cache")
-    _expect(slots, "slots", torch.int64, (tokens,))
-    q_heads, qs, qos = 0, 0, 0
-    if q is not None:
-        qs = _heads_of(q, "q")
-        if q.shape[0] != tokens or q.shape[2] != d:
-            raise ValueError("q must be [tokens][q_heads][head_dim]")
-        q_heads = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        qos = _heads_of(q_out, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rot = 0
-    if turns is not None:
-        _expect(turns, "turns", torch.int64)
-        rot = 2 * turns.numel()
-        if positions is None and rot:
-            raise ValueError("turns without positions")
-    if positions is not None:
-        _expect(positions, "positions", torch.int32, (tokens,))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _expect(w, name, torch.bfloat16, (d,))
-    dev = k.get_device()
-    if dev < 0:
-        raise ValueError("k must be a CUDA tensor (this library has no CPU path)")
-    _paged_on(dev, q, v, slots, k_cache, v_cache, k_scales, v_scales, positions, turns, q_weight, k_weight, q_out)
-    _call_on(dev, "fp8_kv_append", cache, None if q is None else q.data_ptr(), qs, q_heads, k.data_ptr(), ks,
-             v.data_ptr(), vs, tokens, slots.data_ptr(), None if positions is None else positions.data_ptr(),
-             None if turns is None else turns.data_ptr(), rot, 1 if interleaved else 0, gain,
-             None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
-             None if q_out is None else q_out.data_ptr(), qos)
-    return q_out
+    return (_calls or _load_calls()).append(q, k, v, slots, k_cache, v_cache, k_scales, v_scales, fmt, gran, positions, turns,
+                                            interleaved, gain, q_weight, k_weight, eps, q_out)
 
 
-@functools.lru_cache(maxsize=1024)
 def attention_workspace_bytes(batch: int, max_tokens: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     """Workspace bytes of fp8_attention_paged; max_tokens = max_pages * page_size."""
     return int(lib().fp8q_attention_workspace_bytes(batch, max_tokens, q_heads, kv_heads, head_dim))
@@ -967,32 +846,5 @@ def fp8_attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     int32 [batch] (the new token included).  window > 0: only the last `window` tokens and the first
     `sinks` are visible.  scale: head_dim ** -0.5 when not given.  ws: scratch, allocated when not
     given (so calls on different streams or in different graphs never share one)."""
-    qs = _heads_of(q, "q")
-    cache = _pages_struct(k_cache, v_cache, k_scales, v_scales, fmt, gran)
-    batch, q_heads, d = q.shape
-    heads = cache.heads
-    if d != cache.head_dim or q_heads == 0 or heads == 0 or q_heads % heads:
-        raise ValueError("q must be [batch][q_heads][head_dim] with q_heads a multiple of the cache's heads")
-    _expect(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError("block_table must be [batch][max_pages]")
-    _expect(lens, "lens", torch.int32, (batch,))
-    if out is None:
-        out = torch.empty((batch, q_heads, d), dtype=torch.bfloat16, device=q.device)
-    os_ = _heads_of(out, "out")
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if lse is None:
-        lse = torch.empty((batch, q_heads), dtype=torch.float32, device=q.device)
-    _expect(lse, "lse", torch.float32, (batch, q_heads))
-    dev = q.get_device()
-    if dev < 0:
-        raise ValueError("q must be a CUDA tensor (this library has no CPU path)")
-    _paged_on(dev, k_cache, v_cache, k_scales, v_scales, block_table, lens, out, lse, ws)
-    max_pages = block_table.shape[1]
-    nbytes = attention_workspace_bytes(batch, max_pages * cache.page_size, q_heads, heads, d)
-    ws = _workspace(nbytes, q.device, ws)
-    _call_on(dev, "fp8_attention_paged", cache, q.data_ptr(), qs, q_heads, block_table.data_ptr(), batch, max_pages,
-             lens.data_ptr(), d ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), os_, lse.data_ptr(),
-             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
-    return out, lse
+    return (_calls or _load_calls()).attention(q, k_cache, v_cache, k_scales, v_scales, fmt, gran, block_table, lens, scale,
+                                               window, sinks, out, lse, ws)

@@ -4,6 +4,7 @@
 
 Each .cu under csrc/ compiles to an object under _build/ (in parallel, only when the source
 or a header is newer), then all objects link into fp8_quantization_amax_b200/libfp8q.so.
+csrc/torch_calls.cpp, the paged calls' checks against torch's headers, becomes _torch_calls.so.
 IEEE division and square root and no flush-to-zero: the quantizer's contract is bit-exact.
 """
 from __future__ import annotations
@@ -13,6 +14,7 @@ import os
 import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +22,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8q.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 NVCC_FLAGS = [
@@ -60,6 +63,38 @@ def _check_register_split(ptxas_report: str) -> None:
                                f"split needs exactly {GEMM_LAUNCH_REGS}")
 
 
+def _build_calls(force: bool, verbose: bool) -> None:
+    """_torch_calls.so: rebuilt when its source, the C header, torch or Python changes."""
+    import torch
+    src = os.path.join(CSRC, "torch_calls.cpp")
+    stamp = os.path.join(BUILD, "torch_calls_for.txt")
+    made_for = f"torch {torch.__version__} python {sysconfig.get_config_var('SOABI')}"
+    try:
+        with open(stamp) as f:
+            same = f.read() == made_for
+    except OSError:
+        same = False
+    if not force and same and os.path.exists(CALLS) and \
+            os.path.getmtime(CALLS) >= max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "fp8q.h"))):
+        return
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include") if os.path.isabs(_nvcc()) else "/usr/local/cuda/include"
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", cuda, "-I", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    with open(stamp, "w") as f:
+        f.write(made_for)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -86,8 +121,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 raise
         return obj
 
-    with ThreadPoolExecutor(max(1, min(len(sources), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max(1, min(len(sources) + 1, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_build_calls, force, verbose)
         objs = list(ex.map(compile_one, sources))
+        calls.result()
     # the objects the library was last linked from: a source removed or added relinks it even
     # when every remaining object is older than the library
     stamp = os.path.join(BUILD, "linked_objects.txt")
