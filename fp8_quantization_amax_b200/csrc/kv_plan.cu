@@ -7,9 +7,11 @@
 // microsecond of traffic at most: the chain of dependent steps (lengths, two sums, table, slots)
 // and the launches are what a call costs.
 //
-// One block of 1024 threads does the requests (kChunk at a time).  Up to kInlineTokens tokens it
-// goes on to the slots itself; above that a second launch over the whole machine does, from the
-// per-request plan left in the workspace.
+// One block of 1024 threads does the requests (kChunk at a time): one sum over the pages given back
+// and the new tokens, one over the pages wanted.  Up to kInlineTokens tokens it goes on to the slots
+// itself; above that a second launch over the whole machine does, from the per-request plan left in
+// the workspace.  There a warp looks up the requests of its first and last token by 32-way
+// searches (two dependent loads for 1024 requests), and its threads search between them.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,6 +27,7 @@ namespace plan {
 constexpr int kChunk = 1024;
 constexpr int kInlineTokens = 4096;
 constexpr int kSpreadThreads = 256;
+constexpr int kSpreadTokens = 4;             // of a thread
 
 struct Request {
   int old_len;     // tokens held before
@@ -57,7 +60,32 @@ __device__ __forceinline__ int pages_of(int64_t tokens, const Params& p) {
   return (int)((tokens + p.page_size - 1) / p.page_size);
 }
 
-// inclusive sum over the block's threads; *all: the block's sum
+// inclusive sums over the block's threads; *all: the block's sums
+struct Pair {
+  int64_t x, y;
+};
+__device__ __forceinline__ Pair block_sum(Pair v, Pair* sh, Pair* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, v.x, o), y = __shfl_up_sync(0xFFFFFFFFu, v.y, o);
+    if (lane >= o) v.x += x, v.y += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = v;
+  __syncthreads();
+  Pair w = sh[lane];                         // the warps' sums, summed up by every warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, w.x, o), y = __shfl_up_sync(0xFFFFFFFFu, w.y, o);
+    if (lane >= o) w.x += x, w.y += y;
+  }
+  all->x = __shfl_sync(0xFFFFFFFFu, w.x, 31);
+  all->y = __shfl_sync(0xFFFFFFFFu, w.y, 31);
+  const int64_t x = __shfl_sync(0xFFFFFFFFu, w.x, (warp + 31) & 31), y = __shfl_sync(0xFFFFFFFFu, w.y, (warp + 31) & 31);
+  if (warp > 0) v.x += x, v.y += y;
+  return v;
+}
 __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh, int64_t* all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -68,21 +96,20 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh, int64_t* al
   __syncthreads();
   if (lane == 31) sh[warp] = v;
   __syncthreads();
-  int64_t before = 0, total = 0;
+  int64_t w = sh[lane];
 #pragma unroll
-  for (int k = 0; k < kChunk / 32; ++k) {
-    const int64_t x = sh[k];
-    if (k < warp) before += x;
-    total += x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, w, o);
+    if (lane >= o) w += up;
   }
-  *all = total;
-  return v + before;
+  *all = __shfl_sync(0xFFFFFFFFu, w, 31);
+  const int64_t before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) & 31);
+  return warp > 0 ? v + before : v;
 }
 
-// largest i in [0, n) with first[i] <= x (first[0] <= x)
+// largest i in [lo, hi) with first[i] <= x (first[lo] <= x)
 template <class T>
-__device__ __forceinline__ int find(const T* first, int n, T x) {
-  int lo = 0, hi = n;
+__device__ __forceinline__ int find(const T* first, int lo, int hi, T x) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= x) lo = mid;
@@ -91,11 +118,22 @@ __device__ __forceinline__ int find(const T* first, int n, T x) {
   return lo;
 }
 
-// slot and position of token i, and the table entry where it is the first of a new page
-__device__ __forceinline__ void place_token(const Params& p, int i, const int* offsets, const Request* plan, int total) {
-  const int b = find(offsets, p.batch, i);
-  const Request r = plan[b];
-  const int64_t pos = (int64_t)r.old_len + (i - offsets[b]);
+// The same in [0, n) by a whole warp, 32 places at a time.
+__device__ __forceinline__ int find_by_warp(const int* first, int n, int x) {
+  int lo = 0, hi = n;                        // the answer lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int span = (hi - lo + 31) / 32, at = lo + (int)(threadIdx.x & 31) * span;
+    const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < hi && first[at] <= x);
+    lo += (31 - __clz(below | 1u)) * span;
+    hi = min(hi, lo + span);
+  }
+  return lo;
+}
+
+// slot and position of token i of request b, whose first one is `first`, and the table entry where it
+// is the first of a new page
+__device__ __forceinline__ void place_token(const Params& p, int i, int b, int first, const Request& r, int total) {
+  const int64_t pos = (int64_t)r.old_len + (i - first);
   int64_t slot = -1;
   if (r.from >= 0) {
     const int col = (int)div_u32((uint32_t)pos, p.page_div);
@@ -116,43 +154,68 @@ __device__ __forceinline__ void place_token(const Params& p, int i, const int* o
 }
 
 __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
+  __shared__ Pair sh_pair[kChunk / 32];
   __shared__ int64_t sh[kChunk / 32];
-  __shared__ int first[kChunk + 1];          // first given-back page, later first token, of each request
+  __shared__ int first[kChunk];              // first given-back page of each request that ends; first token of each
+  __shared__ int ending[kChunk];             // requests that end
   __shared__ Request sh_plan[kChunk];
+  __shared__ int sh_used;
   const int tid = threadIdx.x;
+  if (tid == 0) sh_used = 0;
   allow_dependent_launch();
   grid_dependency_wait();
 
   int count = *p.free_count;
+  const int64_t row_tokens = (int64_t)p.max_pages * p.page_size;
   if (count < 0 || count > p.num_pages) {
     if (tid == 0) raise_device_error(p.err, kErrBadPage);
     count = max(0, min(count, p.num_pages));
   }
-  const int64_t row_tokens = (int64_t)p.max_pages * p.page_size;
+  int64_t total = count, tokens = 0;
 
-  // ---- requests that end: their pages go on the free list, in order
-  int64_t total = count;
-  for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
-    const int b = b0 + tid;
-    int64_t back = 0;
+  struct Row {
+    int64_t len, more;                       // tokens held and new
+    bool ends;
+  };
+  auto row = [&](int b, bool report) {
+    Row r = {0, 0, false};
     if (b < p.batch) {
-      const int64_t len = p.lens[b];
-      if (len < 0 || len > row_tokens) raise_device_error(p.err, kErrBadPage);
-      if (p.added[b] < 0) back = pages_of(max((int64_t)0, min(len, row_tokens)), p);
+      const int len = p.lens[b], n = p.added[b];
+      if (report && (len < 0 || len > row_tokens)) raise_device_error(p.err, kErrBadPage);
+      r.len = max((int64_t)0, min((int64_t)len, row_tokens));
+      r.ends = n < 0;
+      r.more = max(0, n);
     }
-    int64_t all;
-    const int64_t incl = block_sum(back, sh, &all);
-    if (all == 0) continue;                  // the same for every thread
+    return r;
+  };
+
+  // ---- requests that end: their pages go on the free list, in order.  The sums: pages given back
+  // (x, less than 2^31 in all) with the number of requests that give some above bit 32, new tokens (y)
+  Row r;
+  int64_t end = 0;                           // this thread's request's last token + 1 among the new ones
+  for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
+    r = row(b0 + tid, true);
+    const int back = r.ends ? pages_of(r.len, p) : 0;
+    Pair all;
+    const Pair upto = block_sum(Pair{back > 0 ? (int64_t(1) << 32) | back : 0, r.more}, sh_pair, &all);
+    end = tokens + upto.y;
+    if (p.batch > kChunk) tokens = 0;        // summed up again below
+    else tokens = all.y;
+    const int given = (int)(uint32_t)all.x, givers = (int)(all.x >> 32);
+    if (given == 0) continue;                // the same for every thread
+    if (back > 0) {
+      const int k = (int)(upto.x >> 32) - 1;
+      first[k] = (int)(uint32_t)upto.x - back;
+      ending[k] = b0 + tid;
+    }
     int64_t room = (int64_t)p.num_pages - total;
-    if (all > room && tid == 0) raise_device_error(p.err, kErrBadPage);
-    if (all < room) room = all;              // what does not fit on the list is dropped
-    first[tid] = (int)(incl - back);         // at most the table's entries: checked on the host
+    if (given > room && tid == 0) raise_device_error(p.err, kErrBadPage);
+    if (given < room) room = given;          // what does not fit on the list is dropped
     __syncthreads();
-    const int nb = min(kChunk, p.batch - b0);
-    for (int i = tid; i < room; i += kChunk) {
-      // among requests that start at the same page (all but the last give none back) the last
-      const int r = find(first, nb, i);
-      p.free[total + i] = p.table[(int64_t)(b0 + r) * p.max_pages + (i - first[r])];
+#pragma unroll 4
+    for (int i = tid; i < (int)room; i += kChunk) {
+      const int k = find(first, 0, givers, i);
+      p.free[total + i] = p.table[(int64_t)ending[k] * p.max_pages + (i - first[k])];
     }
     total += room;
     __syncthreads();
@@ -160,46 +223,41 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
   __syncthreads();                           // the list is complete
 
   // ---- the others: pages wanted, served in order while they last
-  int64_t wanted = 0, tokens = 0, used = 0;
+  int64_t wanted = 0, used = 0;
   for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
     const int b = b0 + tid;
-    int64_t len = 0, more = 0, need = 0;
-    bool fits = false, ends = false;
-    if (b < p.batch) {
-      len = max((int64_t)0, min((int64_t)p.lens[b], row_tokens));
-      const int n = p.added[b];
-      ends = n < 0;
-      more = max(0, n);
-      fits = !ends && len + more <= row_tokens;
-    }
     int64_t all;
-    const int64_t end = tokens + block_sum(more, sh, &all);
-    tokens += all;
-    fits = fits && end <= p.max_tokens;
-    if (fits) need = pages_of(len + more, p) - pages_of(len, p);
+    if (p.batch > kChunk) {
+      r = row(b, false);
+      end = tokens + block_sum(r.more, sh, &all);
+      tokens += all;
+    }
+    int64_t need = 0;
+    const bool fits = b < p.batch && !r.ends && r.len + r.more <= row_tokens && end <= p.max_tokens;
+    if (fits) need = pages_of(r.len + r.more, p) - pages_of(r.len, p);
     const int64_t upto = wanted + block_sum(need, sh, &all);
     wanted += all;
     const bool ok = fits && (need == 0 || upto <= total);
     if (b < p.batch) {
-      const Request r = {(int)len, ok ? (int)(upto - need) : -1};
-      if (p.plan) p.plan[b] = r;
-      else sh_plan[tid] = r;
-      const int off = (int)min(end - more, (int64_t)0x7FFFFFFF);
-      if (!p.plan) first[tid] = off;
+      const Request q = {(int)r.len, ok ? (int)(upto - need) : -1};
+      const int off = (int)min(end - r.more, (int64_t)0x7FFFFFFF);
+      if (p.plan) {
+        p.plan[b] = q;
+      } else {
+        sh_plan[tid] = q;
+        first[tid] = off;
+      }
       p.offsets[b] = off;
       p.served[b] = ok ? 1 : 0;
-      p.lens_out[b] = (int)(ends ? 0 : ok ? len + more : len);
+      p.lens_out[b] = (int)(r.ends ? 0 : ok ? r.len + r.more : r.len);
     }
-    // the pages of the served requests are the first `used`: upto grows with b
-    const int64_t mine = ok ? upto : 0;
-    int64_t top = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    __syncthreads();
-    if ((tid & 31) == 0) sh[tid >> 5] = top;
-    __syncthreads();
-    for (int k = 0; k < kChunk / 32; ++k) used = max(used, sh[k]);
+    // the pages of the served requests are the first `used`: upto grows with b, and is at most total
+    // (below 2^31) where a request that needs pages is served
+    const int top = __reduce_max_sync(0xFFFFFFFFu, ok && need > 0 ? (int)upto : 0);
+    if ((tid & 31) == 0 && top > 0) atomicMax(&sh_used, top);
   }
+  __syncthreads();
+  used = sh_used;
   if (tid == 0) {
     p.offsets[p.batch] = (int)min(tokens, (int64_t)0x7FFFFFFF);
     *p.free_count_out = (int)(total - used);
@@ -208,11 +266,12 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
   if (!p.inline_tokens) return;
 
   // ---- slots and positions
-  __syncthreads();
   const int n = (int)min(tokens, (int64_t)p.max_tokens);
+#pragma unroll 2
   for (int i = tid; i < p.max_tokens; i += kChunk) {
     if (i < n) {
-      place_token(p, i, first, sh_plan, (int)total);
+      const int b = find(first, 0, p.batch, i);
+      place_token(p, i, b, first[b], sh_plan[b], (int)total);
     } else {
       p.slots[i] = -1;
       p.positions[i] = 0;
@@ -223,14 +282,25 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
 __global__ void __launch_bounds__(kSpreadThreads) k_pages_spread(const Params p) {
   allow_dependent_launch();
   grid_dependency_wait();
-  const int n = p.offsets[p.batch];
-  const int i = blockIdx.x * kSpreadThreads + threadIdx.x;
-  if (i >= p.max_tokens) return;
-  if (i < n) {
-    place_token(p, i, p.offsets, p.plan, *p.total);
-  } else {
-    p.slots[i] = -1;
-    p.positions[i] = 0;
+  const int n = min(p.offsets[p.batch], p.max_tokens), total = *p.total;
+  const int lane = threadIdx.x & 31;
+  const int64_t begin = ((int64_t)blockIdx.x * (kSpreadThreads / 32) + (threadIdx.x >> 5)) * (32 * kSpreadTokens);
+  if (begin >= p.max_tokens) return;
+  int lo = 0, hi = 0;
+  if (begin < n) {
+    lo = find_by_warp(p.offsets, p.batch, (int)begin);
+    hi = find_by_warp(p.offsets, p.batch, (int)min(begin + 32 * kSpreadTokens, (int64_t)n) - 1);
+  }
+#pragma unroll
+  for (int k = 0; k < kSpreadTokens; ++k) {
+    const int64_t i = begin + 32 * k + lane;
+    if (i < n) {
+      const int b = find(p.offsets, lo, hi + 1, (int)i);
+      place_token(p, (int)i, b, p.offsets[b], p.plan[b], total);
+    } else if (i < p.max_tokens) {
+      p.slots[i] = -1;
+      p.positions[i] = 0;
+    }
   }
 }
 
@@ -271,7 +341,8 @@ cudaError_t launch_pages_update(const PagesUpdate& u, cudaStream_t st) {
   p.err = device_error_word();
   const cudaError_t e = launch_pdl(plan::k_pages_plan, dim3(1), dim3(plan::kChunk), 0, st, p);
   if (e != cudaSuccess || p.inline_tokens) return e;
-  const int blocks = (int)((u.max_tokens + plan::kSpreadThreads - 1) / plan::kSpreadThreads);
+  const int64_t per_block = plan::kSpreadThreads * plan::kSpreadTokens;
+  const int blocks = (int)((u.max_tokens + per_block - 1) / per_block);
   return launch_pdl(plan::k_pages_spread, dim3(blocks), dim3(plan::kSpreadThreads), 0, st, p);
 }
 

@@ -606,6 +606,19 @@ def test_pages_tokens_beyond_max_tokens_are_not_served():
     assert host(got[3]).tolist() == [1, 0, 0]
 
 
+@pytest.mark.parametrize("B", [3, 1300])
+def test_pages_of_a_request_that_is_not_served_stay_free(B):
+    """A request without enough pages, then one that needs none: what is on the list stays there."""
+    free = np.arange(20, dtype=np.int32)
+    table, lens = np.zeros((B, 6), np.int32), np.zeros(B, np.int32)
+    table[0, 0], table[B - 1, 0], lens[0], lens[B - 1] = 18, 19, 3, 1
+    plain = ref.Pages(table, lens, free, 2, 4)
+    added = np.zeros(B, np.int32)
+    added[0], added[B - 1] = 20, 2
+    got = check_step(plain, device_pages(table, lens, free, 2), added, 22, 4)
+    assert int(host(got[5])[0]) == 2 and host(got[3])[[0, B - 1]].tolist() == [0, 1]
+
+
 def test_pages_nothing_and_empty():
     free, count = torch.arange(4, dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
     e = torch.empty(0, dtype=torch.int32, device="cuda")
