@@ -50,10 +50,11 @@ namespace attn {
 constexpr int kMaxWarps = 16;
 constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
 constexpr int kMinTiles = 4;
+constexpr int64_t kMaxTiles = 0x7FFFFFFF;      // of all requests
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
-constexpr int kJoinBatch = 4;                 // parts whose loads are in flight together
+constexpr int kJoinBatch = 8;                 // parts whose loads are in flight together
 constexpr float kSlack = 8.0f;                // a score may exceed the running maximum by this (base 2)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -127,14 +128,24 @@ __device__ __forceinline__ float lds32(uint32_t addr) {
   return v;
 }
 
+// 2^x.  Results below 2^-126 become zero unless FULL: that takes four instructions in place of one.
+// Without scales of single tokens the largest weight of a row is at least 2^-kSlack and what
+// vanishes does not show; a token's scale joins the reference, so with them all weights may be small.
+template <bool FULL>
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  if constexpr (FULL) asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  else asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2_normal(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // 8 x 8 f16: lane holds row lane / 4, columns 2 (lane % 4) + {0, 1}; the same of the transposed matrix
@@ -151,7 +162,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // 2^(a - b) with b = -inf standing for "nothing yet" (a is -inf too then)
-__device__ __forceinline__ float ex2_diff(float a, float b) { return b == -INFINITY ? 0.0f : ex2(a - b); }
+template <bool FULL>
+__device__ __forceinline__ float ex2_diff(float a, float b) {
+  return b == -INFINITY ? 0.0f : ex2<FULL>(a - b);
+}
 
 __device__ __forceinline__ int clamped_len(const Params& p, int b) {
   const int n = __ldg(p.lens + b);
@@ -210,12 +224,13 @@ struct State {
     }
   }
   // add the heads of tile n over other tokens
+  template <bool FULL>
   __device__ __forceinline__ void add_tile(int n, const float* image, int lane) {
     const float2 um = *reinterpret_cast<const float2*>(image + 128 * kDimTiles + 2 * (lane & 3));
     const float2 ul = *reinterpret_cast<const float2*>(image + 128 * kDimTiles + 8 + 2 * (lane & 3));
     const float m0 = fmaxf(m[n][0], um.x), m1 = fmaxf(m[n][1], um.y);
-    const float u0 = ex2_diff(um.x, m0), u1 = ex2_diff(um.y, m1);
-    rescale(n, ex2_diff(m[n][0], m0), ex2_diff(m[n][1], m1));
+    const float u0 = ex2_diff<FULL>(um.x, m0), u1 = ex2_diff<FULL>(um.y, m1);
+    rescale(n, ex2_diff<FULL>(m[n][0], m0), ex2_diff<FULL>(m[n][1], m1));
     m[n][0] = m0;
     m[n][1] = m1;
     l[n][0] += ul.x * u0;
@@ -286,21 +301,24 @@ __host__ __device__ constexpr int stages_of(int dp, int nh) {
              ? 204800 / (warps_of(dp, nh) * (2 * kAttnTile * dp + 2 * kAttnTile * 4)) : 6;
 }
 
-// Sum over the threads up to and including this one, and over the block
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh, int64_t* all) {
+// Sum over the threads up to and including this one, and over the block (in *any: is `flag` set in any
+// thread).  sh: kMaxWarps entries that no thread still reads
+__device__ __forceinline__ int block_sum(int v, bool flag, int* sh, int* all, bool* any) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += up;
   }
-  __syncthreads();                           // sh of the call before has been read
   if (lane == 31) sh[warp] = v;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int k = 0; k < (int)(blockDim.x >> 5); ++k) {
-    if (k < warp) before += sh[k];
-    total += sh[k];
+  *any = __syncthreads_or(flag) != 0;
+  const int warps = blockDim.x >> 5;
+  int before = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxWarps; ++k) {
+    const int x = k < warps ? sh[k] : 0;
+    if (k < warp) before += x;
+    total += x;
   }
   *all = total;
   return v + before;
@@ -339,9 +357,8 @@ __device__ __forceinline__ void advance(const Params& p, Cursor& c) {
 template <int FMT, int DP, int NH, bool TOKEN_SCALES>
 __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Params p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t sh_sum[kMaxWarps];
-  __shared__ int64_t sh_base;
-  __shared__ int sh_req;
+  __shared__ __align__(16) int sh_sum[2][kMaxWarps];
+  __shared__ int sh_base, sh_req;
   __shared__ int sh_free[kMaxWarps];         // each warp's free stage at a request's end
   constexpr int DPC = DP / 16;               // 16-byte pieces of a padded row
   constexpr int RPI = 32 / DPC;              // rows one warp-wide copy covers
@@ -366,24 +383,24 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   grid_dependency_wait();
 
   // ---- total number of tiles; this block's share of them, and the request it begins in.  With at
-  // most one request a thread one sum over the block gives all.  Requests without a visible token
-  // are counted from bit 48 on.
-  constexpr int64_t kOneEmpty = int64_t(1) << 48;
+  // most one request a thread one sum over the block gives all.
   const bool single = p.batch <= (int)blockDim.x;
-  int64_t mine = 0;
+  int mine = 0;
+  bool empty = false;
   for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
     const int n = attn_range(clamped_len(p, b), p.window, p.sinks).tiles;
-    mine += n == 0 ? kOneEmpty : n;
+    mine += n;
+    empty |= n == 0;
   }
-  int64_t all;
-  const int64_t upto = block_sum(mine, sh_sum, &all) & (kOneEmpty - 1);
-  const int64_t total = all & (kOneEmpty - 1);
+  int total;
+  bool any_empty;
+  const int upto = block_sum(mine, empty, sh_sum[0], &total, &any_empty);
   const int workers = attn_workers(total, p.workers, kMinTiles);
   const int w = blockIdx.x;
   if (blockIdx.y == 0 && threadIdx.x == 0 && p.desc) p.desc[w] = make_int4(-1, 0, 0, 0);
 
   // requests without a visible token: zeros, and an empty sum
-  if (all >= kOneEmpty) {
+  if (any_empty) {
     for (int b = w; b < p.batch; b += p.workers) {
       if (clamped_len(p, b) > 0) continue;
       if (active && phase == 0) {
@@ -396,19 +413,21 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
     }
   }
   if (w >= workers || total == 0) return;
-  const int64_t t_begin = attn_start(total, workers, w), t_end = attn_start(total, workers, w + 1);
+  const AttnSplit split = attn_split(total, workers);
+  const int t_begin = attn_start(split, w), t_end = attn_start(split, w + 1);
   if (single) {
-    const int64_t tiles = mine & (kOneEmpty - 1);
-    if (tiles > 0 && upto - tiles <= t_begin && t_begin < upto) {
+    if (mine > 0 && upto - mine <= t_begin && t_begin < upto) {
       sh_req = threadIdx.x;
-      sh_base = upto - tiles;
+      sh_base = upto - mine;
     }
   } else {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
+    int before = 0;
+    for (int b0 = 0, turn = 1; b0 < p.batch; b0 += blockDim.x, turn ^= 1) {
       const int b = b0 + threadIdx.x;
-      const int64_t n = b < p.batch ? attn_range(clamped_len(p, b), p.window, p.sinks).tiles : 0;
-      const int64_t incl = before + block_sum(n, sh_sum, &all);
+      const int n = b < p.batch ? attn_range(clamped_len(p, b), p.window, p.sinks).tiles : 0;
+      int all;
+      bool any;
+      const int incl = before + block_sum(n, false, sh_sum[turn], &all, &any);
       if (n > 0 && incl - n <= t_begin && t_begin < incl) {
         sh_req = b;
         sh_base = incl - n;
@@ -441,8 +460,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
 
   Cursor load, c;                            // of the copies, and of the products
   c.b = sh_req;
-  c.left = (int)(t_end - t_begin);
-  enter(p, c, (int)(t_begin - sh_base));
+  c.left = t_end - t_begin;
+  enter(p, c, t_begin - sh_base);
   load = c;
 
   auto tile_token = [&](int i, int n) {
@@ -462,25 +481,37 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + r0) * D) + lane * 128);
   };
 
-  // ---- copies: `i_load` is the next tile to copy, `page` the page of this lane's token of it
-  // (lane % 16, or the tile's) or -1 where there is none
-  int i_load = load.first + phase, page = -1, tok_load = 0;
-  auto find_page = [&]() {
+  // ---- copies: `i_load` is the next tile to copy.  Where a tile lies in one page, lane l holds the
+  // page of the l-th of the warp's 32 tiles from i_load - used * phases on, else `pages` is the page of
+  // this lane's token (lane % 16) of the next tile; -1 where there is none
+  int i_load = load.first + phase, pages = -1, used = 32;
+  auto page_at = [&](int i, int tok) {
+    return i < load.end && tok < load.n
+               ? __ldg(p.table + (int64_t)load.b * p.max_pages + div_u32((uint32_t)tok, p.c.page_div)) : -1;
+  };
+  auto find_pages = [&]() {
     while (i_load >= load.end && load.b < p.batch) {
       advance(p, load);
       i_load = load.first + phase;
+      used = 32;
       if (load.b < p.batch) prefetch_q(load.b);
     }
-    page = -1;
     if (load.b >= p.batch) return;
-    tok_load = tile_token(i_load, load.n);
-    const int tok = tok_load + (tile_in_page ? 0 : (lane & 15));
-    if (tok < load.n) page = __ldg(p.table + (int64_t)load.b * p.max_pages + div_u32((uint32_t)tok, p.c.page_div));
+    if (!tile_in_page) {
+      pages = page_at(i_load, tile_token(i_load, load.n) + (lane & 15));
+    } else if (used == 32) {
+      // (a place past the request's last tile may be beyond the tokens' range: page_at does not read it)
+      const int i = i_load + lane * p.phases;
+      pages = page_at(i, i < load.end ? tile_token(i, load.n) : 0);
+      used = 0;
+    }
   };
   auto issue = [&](int slot_index) {
     if (load.b < p.batch) {
       const uint32_t dst = ring_u + slot_index * kBytes;
+      const int tok_load = tile_token(i_load, load.n);
       const bool whole = all_visible(tok_load, load.n);
+      const int page = tile_in_page ? __shfl_sync(0xFFFFFFFFu, pages, used) : pages;
       if (tile_in_page && whole && (uint32_t)page < (uint32_t)p.c.num_pages) {
         const int off = tok_load - (int)(div_u32((uint32_t)tok_load, p.c.page_div) * (uint32_t)p.c.page_size);
         if (has_piece) {
@@ -529,30 +560,18 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         }
       }
       i_load += p.phases;
+      ++used;
     }
     cp_async_commit();
   };
 
-  prefetch_q(c.b);
-  find_page();
-#pragma unroll
-  for (int k = 0; k < kStages - 1; ++k) {
-    issue(k);
-    find_page();
-  }
-  int stage = 0;                             // the next stage to be read; the one before it is free
-
-  while (c.b < p.batch) {
-    const int b = c.b, n = c.n;
-    // ---- query heads as B fragments: f16 after a power of two that brings a head's largest element to
-    // 2^14 .. 2^15; the inverse power joins the score's factor
-    uint32_t qb[NH][DP / 64][8];
-    float qmul[NH][2];
+  // ---- query heads: 16 dims of a row a thread, of the request c.b
+  uint32_t qb[NH][DP / 64][8];
+  auto load_q = [&](int b) {
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       const int r = r0 + 8 * h + g;
       const uint16_t* src = p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + min(r, p.group - 1)) * D;
-      uint32_t mx = 0;
 #pragma unroll
       for (int j = 0; j < DP / 64; ++j) {
         const int k = t + 4 * j;
@@ -563,8 +582,31 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         }
         qb[h][j][0] = x.x, qb[h][j][1] = x.y, qb[h][j][2] = x.z, qb[h][j][3] = x.w;
         qb[h][j][4] = y.x, qb[h][j][5] = y.y, qb[h][j][6] = y.z, qb[h][j][7] = y.w;
-        mx = absmax_v4(absmax_v4(mx, x), y);
       }
+    }
+  };
+
+  find_pages();
+#pragma unroll 1
+  for (int k = 0; k < kStages - 1; ++k) {
+    issue(k);
+    find_pages();
+  }
+  int stage = 0;                             // the next stage to be read; the one before it is free
+
+  while (c.b < p.batch) {
+    const int n = c.n;
+    load_q(c.b);
+    // ---- query heads as B fragments: f16 after a power of two that brings a head's largest element to
+    // 2^14 .. 2^15; the inverse power joins the score's factor
+    float qmul[NH][2];
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      uint32_t mx = 0;
+#pragma unroll
+      for (int j = 0; j < DP / 64; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = absmax2(mx, qb[h][j][i]);
       mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       mx = absmax2(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
       const uint32_t ex = __float_as_uint(packed_amax_to_f32(mx)) >> 23;   // biased exponent of the largest
@@ -585,7 +627,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       cp_async_wait<kStages - 2>();
       __syncwarp();                          // the stage has landed for every lane; the one before is read out
       issue(stage == 0 ? kStages - 1 : stage - 1);
-      find_page();
+      find_pages();
       const uint32_t ks = ring_u + stage * kBytes;
       const uint32_t vs = ks + kAttnTile * DP;
       const uint32_t sc = vs + kAttnTile * DP;
@@ -622,7 +664,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         for (int k = 0; k < 2; ++k) {
           const float kf = lds32(sc + 4 * (g + 8 * k));
           vf[k] = lds32(sc + 4 * (16 + g + 8 * k));
-          vl[k] = lg2(fmaxf(vf[k], 0x1.0p-60f));
+          vl[k] = lg2_normal(fmaxf(vf[k], 0x1.0p-60f));
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             st[h][2 * k] *= kf;
@@ -656,7 +698,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
             for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], d));
             top[e] = fmaxf(top[e], s.m[h][e]);
           }
-          s.rescale(h, ex2_diff(s.m[h][0], top[0]), ex2_diff(s.m[h][1], top[1]));
+          s.rescale(h, ex2_diff<TOKEN_SCALES>(s.m[h][0], top[0]), ex2_diff<TOKEN_SCALES>(s.m[h][1], top[1]));
           s.m[h][0] = top[0];
           s.m[h][1] = top[1];
         }
@@ -667,7 +709,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         const float m0 = s.m[h][0] == -INFINITY ? 0.0f : s.m[h][0], m1 = s.m[h][1] == -INFINITY ? 0.0f : s.m[h][1];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float a = ex2(st[h][2 * k] - m0), e = ex2(st[h][2 * k + 1] - m1);
+          float a = ex2<TOKEN_SCALES>(st[h][2 * k] - m0), e = ex2<TOKEN_SCALES>(st[h][2 * k + 1] - m1);
           s.l[h][0] += a;
           s.l[h][1] += e;
           if constexpr (TOKEN_SCALES) a *= vf[k], e *= vf[k];
@@ -723,7 +765,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         if (phase == 0)
           for (int k = 1; k < p.phases; ++k) {
             const int other = warp + k * p.heads_per_block;
-            s.add_tile(h, reinterpret_cast<const float*>(smem + ((size_t)other * kStages + sh_free[other]) * kBytes), lane);
+            s.template add_tile<TOKEN_SCALES>(h, reinterpret_cast<const float*>(smem + ((size_t)other * kStages + sh_free[other]) * kBytes), lane);
           }
         named_barrier(bar, threads);         // the stages are read before they are written again
       }
@@ -734,10 +776,10 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       }
     }
     const bool opens = c.first == 0, closes = c.end == c.tiles;
-    const int place = c.left == (int)(t_end - t_begin) ? 0 : 1;    // the block's first request, or a later one
+    const int place = c.left == t_end - t_begin ? 0 : 1;        // the block's first request, or a later one
     if (phase == 0) {
       if (opens && closes) {
-        write_rows<DP, NH>(p, s, b, vh, vscale, lane);
+        write_rows<DP, NH>(p, s, c.b, vh, vscale, lane);
       } else {
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -745,24 +787,23 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       }
     }
     if (opens && !closes && blockIdx.y == 0 && threadIdx.x == 0)
-      p.desc[w] = make_int4(b, place, w, min(workers - 1, attn_owner(total, workers, t_end - c.left + c.tiles - 1)));
+      p.desc[w] = make_int4(c.b, place, w, min(workers - 1, attn_owner(split, t_end - c.left + c.tiles - 1)));
     advance(p, c);
   }
   cp_async_wait<0>();
 }
 
-// Second launch: adds up the parts of each shared request.  A unit is a quarter of a part of 128
-// dims: two dim tiles of a row tile of one (request, vhead).  Where units are few, several warps
-// share one (each takes every wpu-th part) and are added in shared memory in their order.
+// Second launch: adds up the parts of each shared request.  A unit is one dim tile of a row tile of
+// one (request, vhead), 16 bytes of a part a thread.  Where units are few, several warps share one
+// (each takes every wpu-th part) and are added in shared memory in their order.
 template <int DP, int NH, bool TOKEN_SCALES>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p) {
   using St = State<DP, NH>;
-  constexpr int kPairs = St::kDimTiles / 2;
-  constexpr int kUnits = NH * kPairs;
+  constexpr int kUnits = NH * St::kDimTiles;
   constexpr int VB = DP / 8;
   __shared__ int4 list[kMaxWorkers];
   __shared__ int sh_count[kJoinWarps];
-  __shared__ float sh[kJoinWarps][12][32];
+  __shared__ float sh[kJoinWarps][8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   allow_dependent_launch();
@@ -774,10 +815,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
     const int w = w0 + threadIdx.x;
     const int4 d = w < p.workers ? p.desc[w] : make_int4(-1, 0, 0, 0);
     const uint32_t has = __ballot_sync(0xFFFFFFFFu, d.x >= 0);
-    __syncthreads();
+    if (w0 > 0) __syncthreads();
     if (lane == 0) sh_count[warp] = __popc(has);
     __syncthreads();
     int at = count + __popc(has & ((1u << lane) - 1u));
+#pragma unroll
     for (int k = 0; k < kJoinWarps; ++k) {
       if (k < warp) at += sh_count[k];
       count += sh_count[k];
@@ -785,58 +827,62 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
     if (d.x >= 0) list[at] = d;
   }
   __syncthreads();
-  const int64_t units = (int64_t)count * p.vheads * kUnits;
-  int wpu = 1;                               // warps a unit
-  while (wpu < kJoinWarps && units * (2 * wpu) <= (int64_t)gridDim.x * kJoinWarps) wpu *= 2;
-  const int per_block = kJoinWarps / wpu, mine = warp % wpu;
-  for (int64_t u0 = (int64_t)blockIdx.x * per_block; u0 < units; u0 += (int64_t)gridDim.x * per_block) {
-    const int64_t u = u0 + warp / wpu;
+  // (at most kMaxWorkers requests of 65536 heads: below 2^31)
+  const uint32_t pairs = (uint32_t)count * (uint32_t)p.vheads, units = pairs * kUnits;
+  uint32_t wpu = 1;                          // warps a unit
+  while (wpu < kJoinWarps && units * (2 * wpu) <= gridDim.x * kJoinWarps) wpu *= 2;
+  const uint32_t per_block = kJoinWarps / wpu, mine = warp & (wpu - 1);
+  const int64_t part_floats = (int64_t)p.vheads * St::kImage;      // of one (worker, first or last request)
+  for (uint32_t u0 = blockIdx.x * per_block; u0 < units; u0 += gridDim.x * per_block) {
+    const uint32_t u = u0 + warp / wpu;
     const bool live = u < units;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f, o[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int4 e = make_int4(0, 0, 0, -1);
-    int vh = 0, n = 0, pair = 0;
+    int vh = 0, n = 0, tile = 0;
     if (live) {
-      const int part = (int)(u % kUnits);
-      const int64_t v = u / kUnits;
-      vh = (int)(v % p.vheads);
-      e = list[v / p.vheads];
-      n = part / kPairs;
-      pair = part % kPairs;
-      for (int x0 = e.z + mine; x0 <= e.w; x0 += wpu * kJoinBatch) {
-        float um[kJoinBatch][2], ul[kJoinBatch][2];
-        float4 uo[kJoinBatch][2];
+      const uint32_t part = u % kUnits, v = u / kUnits, r = v / (uint32_t)p.vheads;
+      vh = (int)(v - r * (uint32_t)p.vheads);
+      e = list[r];
+      n = part / St::kDimTiles;
+      tile = part % St::kDimTiles;
+      // a part's rows of this tile; the first worker holds them as its first or its last request's, the
+      // others as their first
+      const float* at = p.part + (int64_t)(2 * (e.z + (int)mine)) * part_floats + vh * St::kImage + n * St::kTileFloats;
+      if (mine == 0) at += e.y * part_floats;
+      for (int x0 = e.z + (int)mine; x0 <= e.w; x0 += wpu * kJoinBatch) {
+        float2 um[kJoinBatch], ul[kJoinBatch];
+        float4 uo[kJoinBatch];
 #pragma unroll
         for (int k = 0; k < kJoinBatch; ++k) {
-          const int x = x0 + k * wpu;
-          um[k][0] = um[k][1] = -INFINITY;
-          ul[k][0] = ul[k][1] = 0.0f;
-          uo[k][0] = uo[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (x <= e.w) {
-            const float* image = p.part + ((int64_t)(2 * x + (x == e.z ? e.y : 0)) * p.vheads + vh) * St::kImage +
-                                 n * St::kTileFloats;
-            const float2 xm = *reinterpret_cast<const float2*>(image + 128 * St::kDimTiles + 2 * t);
-            const float2 xl = *reinterpret_cast<const float2*>(image + 128 * St::kDimTiles + 8 + 2 * t);
-            um[k][0] = xm.x, um[k][1] = xm.y;
-            ul[k][0] = xl.x, ul[k][1] = xl.y;
-            const float4* q = reinterpret_cast<const float4*>(image) + 64 * pair + lane;
-            uo[k][0] = q[0];
-            uo[k][1] = q[32];
+          um[k] = make_float2(-INFINITY, -INFINITY);
+          ul[k] = make_float2(0.0f, 0.0f);
+          uo[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (x0 + k * (int)wpu <= e.w) {
+            um[k] = *reinterpret_cast<const float2*>(at + 128 * St::kDimTiles + 2 * t);
+            ul[k] = *reinterpret_cast<const float2*>(at + 128 * St::kDimTiles + 8 + 2 * t);
+            uo[k] = reinterpret_cast<const float4*>(at)[32 * tile + lane];
+            at += 2 * wpu * part_floats - (x0 + k == e.z ? e.y * part_floats : 0);
           }
         }
+        float a0 = m0, a1 = m1;
+#pragma unroll
+        for (int k = 0; k < kJoinBatch; ++k) a0 = fmaxf(a0, um[k].x), a1 = fmaxf(a1, um[k].y);
+        const float f0 = ex2_diff<TOKEN_SCALES>(m0, a0), f1 = ex2_diff<TOKEN_SCALES>(m1, a1);
+        m0 = a0;
+        m1 = a1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] *= (j & 1) ? f1 : f0;
 #pragma unroll
         for (int k = 0; k < kJoinBatch; ++k) {
-          const float a0 = fmaxf(m0, um[k][0]), a1 = fmaxf(m1, um[k][1]);
-          const float f0 = ex2_diff(m0, a0), f1 = ex2_diff(m1, a1);
-          const float h0 = ex2_diff(um[k][0], a0), h1 = ex2_diff(um[k][1], a1);
-          m0 = a0;
-          m1 = a1;
-          l0 = l0 * f0 + ul[k][0] * h0;
-          l1 = l1 * f1 + ul[k][1] * h1;
-          const float x[8] = {uo[k][0].x, uo[k][0].y, uo[k][0].z, uo[k][0].w, uo[k][1].x, uo[k][1].y, uo[k][1].z, uo[k][1].w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = (j & 1) ? o[j] * f1 + x[j] * h1 : o[j] * f0 + x[j] * h0;
+          const float h0 = ex2_diff<TOKEN_SCALES>(um[k].x, m0), h1 = ex2_diff<TOKEN_SCALES>(um[k].y, m1);
+          l0 += ul[k].x * h0;
+          l1 += ul[k].y * h1;
+          o[0] += uo[k].x * h0;
+          o[1] += uo[k].y * h1;
+          o[2] += uo[k].z * h0;
+          o[3] += uo[k].w * h1;
         }
       }
     }
@@ -847,19 +893,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
       sh[warp][2][lane] = l0;
       sh[warp][3][lane] = l1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sh[warp][4 + j][lane] = o[j];
+      for (int j = 0; j < 4; ++j) sh[warp][4 + j][lane] = o[j];
       __syncthreads();
       if (mine == 0) {
-        for (int k = warp + 1; k < warp + wpu; ++k) {
+#pragma unroll 1
+        for (int k = warp + 1; k < warp + (int)wpu; ++k) {
           const float b0 = sh[k][0][lane], b1 = sh[k][1][lane];
           const float a0 = fmaxf(m0, b0), a1 = fmaxf(m1, b1);
-          const float f0 = ex2_diff(m0, a0), f1 = ex2_diff(m1, a1), h0 = ex2_diff(b0, a0), h1 = ex2_diff(b1, a1);
+          const float f0 = ex2_diff<TOKEN_SCALES>(m0, a0), f1 = ex2_diff<TOKEN_SCALES>(m1, a1), h0 = ex2_diff<TOKEN_SCALES>(b0, a0), h1 = ex2_diff<TOKEN_SCALES>(b1, a1);
           m0 = a0;
           m1 = a1;
           l0 = l0 * f0 + sh[k][2][lane] * h0;
           l1 = l1 * f1 + sh[k][3][lane] * h1;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < 4; ++j)
             o[j] = (j & 1) ? o[j] * f1 + sh[k][4 + j][lane] * h1 : o[j] * f0 + sh[k][4 + j][lane] * h0;
         }
       }
@@ -868,17 +915,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
       float vs = 1.0f;
       if constexpr (!TOKEN_SCALES) vs = __ldg(p.c.vs + (p.c.gran == 0 ? 0 : vh / p.row_tiles));
       const int kvh = vh / p.row_tiles, row = (vh - kvh * p.row_tiles) * 8 * NH + 8 * n + 2 * t;
-      const int dim = g * VB + 4 * pair;     // o holds dims dim .. dim + 3 of rows row, row + 1
+      const int dim = g * VB + 2 * tile;     // o holds dims dim, dim + 1 of rows row, row + 1
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         if (row + r >= p.group) continue;
         const float l = r ? l1 : l0, m = r ? m1 : m0, f = __fdiv_rn(vs, l);
         const int64_t head = kvh * p.group + row + r;
-        if (p.lse && pair == 0 && g == 0)
+        if (p.lse && tile == 0 && g == 0)
           p.lse[(int64_t)e.x * (p.c.heads * p.group) + head] = l == 0.0f ? -INFINITY : kLn2 * (m + lg2(l));
         if (dim < p.c.head_dim)
-          *reinterpret_cast<uint2*>(p.out + (int64_t)e.x * p.out_stride + head * p.c.head_dim + dim) =
-              make_uint2(f32x2_to_bf16x2(o[r] * f, o[2 + r] * f), f32x2_to_bf16x2(o[4 + r] * f, o[6 + r] * f));
+          *reinterpret_cast<uint32_t*>(p.out + (int64_t)e.x * p.out_stride + head * p.c.head_dim + dim) =
+              f32x2_to_bf16x2(o[r] * f, o[2 + r] * f);
       }
     }
   }
@@ -958,29 +1005,31 @@ int check_attention_split(const int* lens, int64_t batch, int window, int sinks,
     total += r.tiles;
   }
   if (total == 0) return 0;
-  const int workers = attn_workers(total, most, attn::kMinTiles);
+  if (total > attn::kMaxTiles) return -1;
+  const int workers = attn_workers((int)total, most, attn::kMinTiles);
   if (workers < 1 || workers > most) return 3;
+  const AttnSplit s = attn_split((int)total, workers);
   int64_t expect = 0;
   for (int w = 0; w < workers; ++w) {
-    if (attn_start(total, workers, w) != expect) return 4;
-    expect = attn_start(total, workers, w + 1);
-    if (expect <= attn_start(total, workers, w)) return 5;       // every worker has work
-    for (int64_t x = attn_start(total, workers, w); x < expect; ++x)
-      if (attn_owner(total, workers, x) != w) return 6;
+    if (attn_start(s, w) != expect) return 4;
+    expect = attn_start(s, w + 1);
+    if (expect <= attn_start(s, w)) return 5;       // every worker has work
+    for (int64_t x = attn_start(s, w); x < expect; ++x)
+      if (attn_owner(s, (int)x) != w) return 6;
   }
   if (expect != total) return 7;
   int64_t base = 0;
   for (int64_t b = 0; b < batch; ++b) {
     const int n = attn_range(lens[b], window, sinks).tiles;
     if (n == 0) continue;
-    const int first = attn_owner(total, workers, base), last = attn_owner(total, workers, base + n - 1);
+    const int first = attn_owner(s, (int)base), last = attn_owner(s, (int)base + n - 1);
     for (int w = first; w <= last; ++w) {
-      const int64_t from = std::max(base, attn_start(total, workers, w));
-      const int64_t to = std::min(base + n, attn_start(total, workers, w + 1));
+      const int64_t from = std::max<int64_t>(base, attn_start(s, w));
+      const int64_t to = std::min<int64_t>(base + n, attn_start(s, w + 1));
       if (from >= to) return 8;                                   // a named worker without a part
       // place 0 is the part at the beginning of a range, place 1 the one at its end
-      const bool at_begin = from == attn_start(total, workers, w);
-      if (first != last && !at_begin && to != attn_start(total, workers, w + 1)) return 9;
+      const bool at_begin = from == attn_start(s, w);
+      if (first != last && !at_begin && to != attn_start(s, w + 1)) return 9;
       if (w > first && !at_begin) return 10;
     }
     base += n;

@@ -49,7 +49,7 @@ __device__ __forceinline__ void cp_async_wait() {
 //
 // A request of n tokens is read in tiles of 16 tokens.  With a window only the tiles that hold a
 // visible token count: those of the first `sinks` tokens and those from token n - window on.  All
-// requests' tiles, laid end to end, are divided evenly over the workers.
+// requests' tiles, laid end to end (below 2^31 of them), are divided evenly over the workers.
 constexpr int kAttnTile = 16;
 
 struct AttnRange {
@@ -76,17 +76,26 @@ __host__ __device__ __forceinline__ AttnRange attn_range(int n, int window, int 
 }
 
 // workers that take part: at least `least` tiles each, so short work is not split without need
-__host__ __device__ __forceinline__ int attn_workers(int64_t tiles, int most, int least) {
-  const int64_t w = (tiles + least - 1) / least;
-  return (int)(w < 1 ? 1 : (w < most ? w : most));
+__host__ __device__ __forceinline__ int attn_workers(int tiles, int most, int least) {
+  const int w = tiles / least + (tiles % least != 0);
+  return w < 1 ? 1 : w < most ? w : most;
 }
 
-// first tile of worker w; the worker that holds tile x
-__host__ __device__ __forceinline__ int64_t attn_start(int64_t tiles, int workers, int w) {
-  return tiles * w / workers;
+// The first `more` workers hold each + 1 tiles, the others each: first tile of worker w, and the worker
+// that holds tile x
+struct AttnSplit {
+  int each, more;
+};
+__host__ __device__ __forceinline__ AttnSplit attn_split(int tiles, int workers) {
+  const int each = (int)((uint32_t)tiles / (uint32_t)workers);
+  return AttnSplit{each, tiles - each * workers};
 }
-__host__ __device__ __forceinline__ int attn_owner(int64_t tiles, int workers, int64_t x) {
-  return (int)(((x + 1) * workers - 1) / tiles);
+__host__ __device__ __forceinline__ int attn_start(const AttnSplit& s, int w) {
+  return w * s.each + (w < s.more ? w : s.more);
+}
+__host__ __device__ __forceinline__ int attn_owner(const AttnSplit& s, int x) {
+  const int front = s.more * (s.each + 1);
+  return x < front ? (int)((uint32_t)x / (uint32_t)(s.each + 1)) : s.more + (int)((uint32_t)(x - front) / (uint32_t)s.each);
 }
 
 }  // namespace fp8q

@@ -74,7 +74,7 @@ def test_bad_caches_are_refused(L, change, status):
     (dict(table=None), 1), (dict(table=MIS4), 1), (dict(q_stride=508), 1), (dict(out_stride=500), 1), (dict(q_stride=256), 1),
     (dict(q_heads=0), 1), (dict(q_heads=7), 1), (dict(batch=-1), 1), (dict(max_pages=-1), 1), (dict(window=-1), 1),
     (dict(sinks=-1), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1),
-    (dict(lse=MIS4), 1), (dict(max_pages=1 << 28), 2), (dict(q_heads=1 << 17), 2), (dict(ws=None, ws_bytes=0), 3),
+    (dict(lse=MIS4), 1), (dict(max_pages=1 << 28), 2), (dict(batch=1 << 12, max_pages=1 << 19), 2), (dict(q_heads=1 << 17), 2), (dict(ws=None, ws_bytes=0), 3),
     (dict(ws_bytes=100), 3), (dict(ws=MIS), 3), (dict(batch=0, q=None, out=None), 0),
 ])
 def test_attention_refuses(L, change, status):
