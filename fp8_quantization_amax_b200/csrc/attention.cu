@@ -155,6 +155,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -259,7 +264,7 @@ __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, in
     for (int e = 0; e < 2; ++e) {
       const int r = r0 + 8 * n + 2 * t + e;
       if (r >= p.group) continue;
-      const float l = s.l[n][e], f = __fdiv_rn(vs, l);
+      const float l = s.l[n][e], f = vs * rcp(l);
       if (p.lse && g == 0)
         p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = l == 0.0f ? -INFINITY : kLn2 * (s.m[n][e] + lg2(l));
       uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D + g * VB;
@@ -919,7 +924,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         if (row + r >= p.group) continue;
-        const float l = r ? l1 : l0, m = r ? m1 : m0, f = __fdiv_rn(vs, l);
+        const float l = r ? l1 : l0, m = r ? m1 : m0, f = vs * rcp(l);
         const int64_t head = kvh * p.group + row + r;
         if (p.lse && tile == 0 && g == 0)
           p.lse[(int64_t)e.x * (p.c.heads * p.group) + head] = l == 0.0f ? -INFINITY : kLn2 * (m + lg2(l));
