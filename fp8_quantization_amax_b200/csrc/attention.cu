@@ -30,9 +30,9 @@
 // [token][head][dim] page is read in whole rows.  With fewer heads than warps several warps take
 // every second, third ... tile of a head and are joined at a request's end through a free stage.
 //
-// All requests' tiles laid end to end are divided evenly over one wave of blocks (kv_pages.cuh), from
-// the lengths on the device: ragged batches and one long request fill the machine alike.  A
-// request whose tiles are shared leaves fp32 partial results, joined by a second launch in the
+// All requests' tiles laid end to end, with what a change of request costs, are divided evenly over
+// one wave of blocks (kv_pages.cuh), from the lengths on the device: ragged batches and one long
+// request fill the machine alike.  A request whose tiles are shared leaves fp32 partial results, joined by a second launch in the
 // blocks' order, so results do not depend on timing.
 #include <cuda_runtime.h>
 
@@ -50,7 +50,8 @@ namespace attn {
 constexpr int kMaxWarps = 16;
 constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
 constexpr int kMinTiles = 4;
-constexpr int64_t kMaxTiles = 0x7FFFFFFF;      // of all requests
+constexpr int64_t kMaxCost = 0x7FFFFFFF;      // of all requests
+constexpr int kTurn = 3;                      // a change of request, in tiles of a phase (see Params::turn)
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
@@ -73,6 +74,7 @@ struct Params {
   float* lse;
   int vheads, row_tiles;     // (key-value head, tile of query rows) pairs; query-row tiles per head
   int heads_per_block, phases;
+  int turn;                  // tiles' worth of a change of request
   int workers;               // gridDim.x of the first launch
   int4* desc;                // per worker: the shared request that begins in its range
   float* part;               // per (worker, first or last request, vhead): a warp's registers
@@ -334,7 +336,7 @@ struct Cursor {
   int b;           // request; the batch size when there is none left
   int n;           // its tokens
   int first, end;  // its tiles [first, end) are the block's
-  int left;        // tiles of the block's share from `first` on
+  int left;        // the block's share from tile `first` on
   int tiles;       // all its tiles
 };
 
@@ -346,7 +348,7 @@ __device__ __forceinline__ void enter(const Params& p, Cursor& c, int first) {
 }
 // to the next request with tiles
 __device__ __forceinline__ void advance(const Params& p, Cursor& c) {
-  c.left -= c.end - c.first;
+  c.left -= c.tiles + p.turn - c.first;
   do {
     ++c.b;
     if (c.left <= 0) c.b = p.batch;
@@ -387,13 +389,13 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   allow_dependent_launch();
   grid_dependency_wait();
 
-  // ---- total number of tiles; this block's share of them, and the request it begins in.  With at
+  // ---- the cost of all requests; this block's share of it, and the request it begins in.  With at
   // most one request a thread one sum over the block gives all.
   const bool single = p.batch <= (int)blockDim.x;
   int mine = 0;
   bool empty = false;
   for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
-    const int n = attn_range(clamped_len(p, b), p.window, p.sinks).tiles;
+    const int n = attn_cost(attn_range(clamped_len(p, b), p.window, p.sinks).tiles, p.turn);
     mine += n;
     empty |= n == 0;
   }
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
     int before = 0;
     for (int b0 = 0, turn = 1; b0 < p.batch; b0 += blockDim.x, turn ^= 1) {
       const int b = b0 + threadIdx.x;
-      const int n = b < p.batch ? attn_range(clamped_len(p, b), p.window, p.sinks).tiles : 0;
+      const int n = b < p.batch ? attn_cost(attn_range(clamped_len(p, b), p.window, p.sinks).tiles, p.turn) : 0;
       int all;
       bool any;
       const int incl = before + block_sum(n, false, sh_sum[turn], &all, &any);
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   c.b = sh_req;
   c.left = t_end - t_begin;
   enter(p, c, t_begin - sh_base);
+  if (c.first >= c.tiles) advance(p, c);     // the share begins behind the request's last tile
   load = c;
 
   auto tile_token = [&](int i, int n) {
@@ -984,19 +987,61 @@ cudaError_t launch_dims(const Params& p, const Shape& s, bool join, cudaStream_t
   return launch<FMT, 256, 1, TOKEN_SCALES>(p, s, join, st);
 }
 
-// No request is shared when a single worker takes all tiles there can be.
+// Can a request be shared?  Not one of a single tile; and the first share, which a lone request begins
+// in, is at least kMinTiles
 inline bool may_share(int64_t batch, int64_t max_tokens) {
-  return batch * ((max_tokens + kAttnTile - 1) / kAttnTile) > kMinTiles;
+  return (max_tokens + kAttnTile - 1) / kAttnTile > (batch == 1 ? kMinTiles : 1);
 }
 
 }  // namespace attn
 
-// Walks every worker's share with the kernel's own functions: each tile of each request is held
-// once, a worker holds parts of at most two shared requests (the first and the last of its range),
-// and the workers named by a shared request's descriptor are those that hold its tiles.
+// Walks every worker's share with the kernel's own functions, for several costs of a change of
+// request: each tile of each request is held once, a worker holds parts of at most two shared
+// requests (the first and the last of its share), the workers named by a shared request's descriptor
+// are those that hold its tiles, and none is shared where the host plans no second launch.
+static int check_split(const int* lens, int64_t batch, int window, int sinks, int most, int turn) {
+  int64_t total = 0;
+  for (int64_t b = 0; b < batch; ++b) total += attn_cost(attn_range(lens[b], window, sinks).tiles, turn);
+  if (total == 0) return 0;
+  if (total > attn::kMaxCost) return -1;
+  const int workers = attn_workers((int)total, most, attn::kMinTiles);
+  if (workers < 1 || workers > most) return 3;
+  const AttnSplit s = attn_split((int)total, workers);
+  int64_t expect = 0;
+  for (int w = 0; w < workers; ++w) {
+    if (attn_start(s, w) != expect) return 4;
+    expect = attn_start(s, w + 1);
+    if (expect <= attn_start(s, w)) return 5;                    // every worker has a share
+    for (int64_t x = attn_start(s, w); x < expect; ++x)
+      if (attn_owner(s, (int)x) != w) return 6;
+  }
+  if (expect != total) return 7;
+  int64_t base = 0;
+  for (int64_t b = 0; b < batch; ++b) {
+    const int n = attn_range(lens[b], window, sinks).tiles;
+    if (n == 0) continue;
+    const int first = attn_owner(s, (int)base), last = attn_owner(s, (int)(base + n - 1));
+    int64_t held = 0;
+    for (int w = first; w <= last; ++w) {
+      // as Cursor's enter() has it: `left` of the share from tile `from` on
+      const int64_t from = std::max<int64_t>(0, attn_start(s, w) - base), left = attn_start(s, w + 1) - base - from;
+      const int64_t to = std::min<int64_t>(n, from + left);
+      if (from != held || from >= to) return 8;                  // a named worker without a part, a tile twice or never
+      held = to;
+      // place 0 is the part at the beginning of a share, place 1 the one at its end
+      const bool at_begin = base + from == attn_start(s, w);
+      if (first != last && !at_begin && base + to != attn_start(s, w + 1)) return 9;
+      if (w > first && !at_begin) return 10;
+    }
+    if (held != n) return 11;
+    if (first != last && !attn::may_share(batch, (int64_t)n * kAttnTile)) return 12;
+    base += attn_cost(n, turn);
+  }
+  return 0;
+}
+
 int check_attention_split(const int* lens, int64_t batch, int window, int sinks, int most) {
   if (batch < 0 || most < 1 || window < 0 || sinks < 0 || (batch > 0 && !lens)) return -1;
-  int64_t total = 0;
   for (int64_t b = 0; b < batch; ++b) {
     const AttnRange r = attn_range(lens[b], window, sinks);
     if (r.tiles < 0 || r.head > r.tiles || r.skip < 0) return 1;
@@ -1007,37 +1052,10 @@ int check_attention_split(const int* lens, int64_t batch, int window, int sinks,
       const int i = tile < r.head ? tile : tile - r.skip;
       if (i < 0 || i >= r.tiles || (i < r.head ? i : i + r.skip) != tile) return 2;
     }
-    total += r.tiles;
   }
-  if (total == 0) return 0;
-  if (total > attn::kMaxTiles) return -1;
-  const int workers = attn_workers((int)total, most, attn::kMinTiles);
-  if (workers < 1 || workers > most) return 3;
-  const AttnSplit s = attn_split((int)total, workers);
-  int64_t expect = 0;
-  for (int w = 0; w < workers; ++w) {
-    if (attn_start(s, w) != expect) return 4;
-    expect = attn_start(s, w + 1);
-    if (expect <= attn_start(s, w)) return 5;       // every worker has work
-    for (int64_t x = attn_start(s, w); x < expect; ++x)
-      if (attn_owner(s, (int)x) != w) return 6;
-  }
-  if (expect != total) return 7;
-  int64_t base = 0;
-  for (int64_t b = 0; b < batch; ++b) {
-    const int n = attn_range(lens[b], window, sinks).tiles;
-    if (n == 0) continue;
-    const int first = attn_owner(s, (int)base), last = attn_owner(s, (int)base + n - 1);
-    for (int w = first; w <= last; ++w) {
-      const int64_t from = std::max<int64_t>(base, attn_start(s, w));
-      const int64_t to = std::min<int64_t>(base + n, attn_start(s, w + 1));
-      if (from >= to) return 8;                                   // a named worker without a part
-      // place 0 is the part at the beginning of a range, place 1 the one at its end
-      const bool at_begin = from == attn_start(s, w);
-      if (first != last && !at_begin && to != attn_start(s, w + 1)) return 9;
-      if (w > first && !at_begin) return 10;
-    }
-    base += n;
+  for (int phases : {1, 2, 5, attn::kMaxWarps}) {
+    const int bad = check_split(lens, batch, window, sinks, most, attn::kTurn * phases);
+    if (bad) return bad;
   }
   return 0;
 }
@@ -1072,6 +1090,7 @@ cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q,
   p.row_tiles = s.row_tiles;
   p.heads_per_block = s.heads_per_block;
   p.phases = s.phases;
+  p.turn = attn::kTurn * s.phases;
   p.workers = s.workers;
   const bool join = attn::may_share(batch, max_pages * c.page_size);
   p.desc = join ? static_cast<int4*>(ws) : nullptr;

@@ -643,8 +643,8 @@ fp8q_status fp8_attention_paged(const fp8q_kv_pages* cache, const void* q, int64
     return FP8Q_ERR_INVALID_ARGUMENT;
   if (q_heads > 65536 || batch > kMaxTableTokens || (max_pages > 0 && cache->page_size > kMaxTableTokens / max_pages))
     return FP8Q_ERR_UNSUPPORTED;
-  // all requests' tiles of 16 tokens are counted in an int
-  if (batch * ((max_pages * cache->page_size + 15) / 16) > kMaxTableTokens) return FP8Q_ERR_UNSUPPORTED;
+  // all requests' tiles of 16 tokens, and up to 48 more for each request, are counted in an int
+  if (batch * ((max_pages * cache->page_size + 15) / 16 + 48) > kMaxTableTokens) return FP8Q_ERR_UNSUPPORTED;
   if (batch == 0) return FP8Q_OK;
   const int64_t row = q_heads * cache->head_dim;
   if (!q || !out || !lens || !aligned(q, 16) || !aligned(out, 16) || !aligned(lens, 4) || q_stride % 8 != 0 ||

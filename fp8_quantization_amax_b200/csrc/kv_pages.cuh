@@ -48,8 +48,10 @@ __device__ __forceinline__ void cp_async_wait() {
 // ---------------------------------------------------------------- division of the attention's work
 //
 // A request of n tokens is read in tiles of 16 tokens.  With a window only the tiles that hold a
-// visible token count: those of the first `sinks` tokens and those from token n - window on.  All
-// requests' tiles, laid end to end (below 2^31 of them), are divided evenly over the workers.
+// visible token count: those of the first `sinks` tokens and those from token n - window on.  A
+// request costs its tiles and `turn` more, what a worker spends on ending one request and beginning
+// the next; all requests' costs, laid end to end (below 2^31 in all), are divided evenly over the
+// workers, and a worker holds the tiles that fall into its share.
 constexpr int kAttnTile = 16;
 
 struct AttnRange {
@@ -75,20 +77,22 @@ __host__ __device__ __forceinline__ AttnRange attn_range(int n, int window, int 
   return r;
 }
 
-// workers that take part: at least `least` tiles each, so short work is not split without need
-__host__ __device__ __forceinline__ int attn_workers(int tiles, int most, int least) {
-  const int w = tiles / least + (tiles % least != 0);
+__host__ __device__ __forceinline__ int attn_cost(int tiles, int turn) { return tiles == 0 ? 0 : tiles + turn; }
+
+// workers that take part: a share of at least `least` each, so short work is not split without need
+__host__ __device__ __forceinline__ int attn_workers(int cost, int most, int least) {
+  const int w = cost / least;
   return w < 1 ? 1 : w < most ? w : most;
 }
 
-// The first `more` workers hold each + 1 tiles, the others each: first tile of worker w, and the worker
-// that holds tile x
+// The first `more` workers' shares are each + 1, the others' each: where worker w's begins, and the worker
+// in whose share place x lies
 struct AttnSplit {
   int each, more;
 };
-__host__ __device__ __forceinline__ AttnSplit attn_split(int tiles, int workers) {
-  const int each = (int)((uint32_t)tiles / (uint32_t)workers);
-  return AttnSplit{each, tiles - each * workers};
+__host__ __device__ __forceinline__ AttnSplit attn_split(int cost, int workers) {
+  const int each = (int)((uint32_t)cost / (uint32_t)workers);
+  return AttnSplit{each, cost - each * workers};
 }
 __host__ __device__ __forceinline__ int attn_start(const AttnSplit& s, int w) {
   return w * s.each + (w < s.more ? w : s.more);

@@ -637,7 +637,7 @@ FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_pages *cache, const void *q, in
  * once and every part is found by the join, a positive code for the first violation, -1 for a bad
  * argument.
  * Requirements: q_heads % heads == 0; q and out 16-byte aligned, strides multiples of 8; scale > 0;
- * batch * max_pages * page_size below 2^35 - 1040.
+ * batch * (max_pages * page_size + 784) below 2^35 - 1040.
  */
 FP8Q_API size_t fp8q_attention_workspace_bytes(int64_t batch, int64_t max_tokens, int64_t q_heads, int64_t kv_heads,
                                                int64_t head_dim);
