@@ -60,51 +60,51 @@ __device__ __forceinline__ int pages_of(int64_t tokens, const Params& p) {
   return (int)((tokens + p.page_size - 1) / p.page_size);
 }
 
-// inclusive sums over the block's threads; *all: the block's sums
+// Inclusive sums over the first n threads of the block; *all: over all of them.  Warps without a value
+// take no part: shuffles of 32 warps would cost more than the steps between them.  sh: that no
+// thread still reads
 struct Pair {
   int64_t x, y;
 };
-__device__ __forceinline__ Pair block_sum(Pair v, Pair* sh, Pair* all) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, v.x, o), y = __shfl_up_sync(0xFFFFFFFFu, v.y, o);
-    if (lane >= o) v.x += x, v.y += y;
-  }
-  __syncthreads();
-  if (lane == 31) sh[warp] = v;
-  __syncthreads();
-  Pair w = sh[lane];                         // the warps' sums, summed up by every warp
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, w.x, o), y = __shfl_up_sync(0xFFFFFFFFu, w.y, o);
-    if (lane >= o) w.x += x, w.y += y;
-  }
-  all->x = __shfl_sync(0xFFFFFFFFu, w.x, 31);
-  all->y = __shfl_sync(0xFFFFFFFFu, w.y, 31);
-  const int64_t x = __shfl_sync(0xFFFFFFFFu, w.x, (warp + 31) & 31), y = __shfl_sync(0xFFFFFFFFu, w.y, (warp + 31) & 31);
-  if (warp > 0) v.x += x, v.y += y;
-  return v;
+__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) { return Pair{a.x + b.x, a.y + b.y}; }
+__device__ __forceinline__ Pair shuffle_up(const Pair& v, int o) {
+  return Pair{__shfl_up_sync(0xFFFFFFFFu, v.x, o), __shfl_up_sync(0xFFFFFFFFu, v.y, o)};
 }
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* sh, int64_t* all) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__device__ __forceinline__ int64_t shuffle_up(int64_t v, int o) { return __shfl_up_sync(0xFFFFFFFFu, v, o); }
+
+template <class T>
+struct Sums {
+  T before[kChunk / 32], all;
+};
+template <class T>
+__device__ __forceinline__ T block_sum(T v, int n, Sums<T>& sh, T* all) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = (n + 31) >> 5;
+  const T own = v;
+  if (warp < warps) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += up;
+    for (int o = 1; o < 32; o <<= 1) {
+      const T up = shuffle_up(v, o);
+      if (lane >= o) v = v + up;
+    }
+    if (lane == 31) sh.before[warp] = v;
   }
   __syncthreads();
-  if (lane == 31) sh[warp] = v;
-  __syncthreads();
-  int64_t w = sh[lane];
+  if (warp == 0) {
+    T w = T{};
+    if (lane < warps) w = sh.before[lane];
+    T upto = w;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, w, o);
-    if (lane >= o) w += up;
+    for (int o = 1; o < 32; o <<= 1) {
+      const T up = shuffle_up(upto, o);
+      if (lane >= o) upto = upto + up;
+    }
+    const T below = shuffle_up(upto, 1);
+    sh.before[lane] = lane == 0 ? T{} : below;
+    if (lane == 31) sh.all = upto;
   }
-  *all = __shfl_sync(0xFFFFFFFFu, w, 31);
-  const int64_t before = __shfl_sync(0xFFFFFFFFu, w, (warp + 31) & 31);
-  return warp > 0 ? v + before : v;
+  __syncthreads();
+  *all = sh.all;
+  return warp < warps ? v + sh.before[warp] : own + sh.all;
 }
 
 // largest i in [lo, hi) with first[i] <= x (first[lo] <= x)
@@ -154,8 +154,8 @@ __device__ __forceinline__ void place_token(const Params& p, int i, int b, int f
 }
 
 __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
-  __shared__ Pair sh_pair[kChunk / 32];
-  __shared__ int64_t sh[kChunk / 32];
+  __shared__ Sums<Pair> sh_pair;
+  __shared__ Sums<int64_t> sh;
   __shared__ int first[kChunk];              // first given-back page of each request that ends; first token of each
   __shared__ int ending[kChunk];             // requests that end
   __shared__ Request sh_plan[kChunk];
@@ -165,13 +165,10 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
   allow_dependent_launch();
   grid_dependency_wait();
 
-  int count = *p.free_count;
+  const int count = *p.free_count;
   const int64_t row_tokens = (int64_t)p.max_pages * p.page_size;
-  if (count < 0 || count > p.num_pages) {
-    if (tid == 0) raise_device_error(p.err, kErrBadPage);
-    count = max(0, min(count, p.num_pages));
-  }
-  int64_t total = count, tokens = 0;
+  int64_t total = max(0, min(count, p.num_pages)), tokens = 0;
+  if (tid == 0 && total != count) raise_device_error(p.err, kErrBadPage);
 
   struct Row {
     int64_t len, more;                       // tokens held and new
@@ -194,10 +191,11 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
   Row r;
   int64_t end = 0;                           // this thread's request's last token + 1 among the new ones
   for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
+    if (b0 > 0) __syncthreads();             // sh_pair has been read
     r = row(b0 + tid, true);
     const int back = r.ends ? pages_of(r.len, p) : 0;
     Pair all;
-    const Pair upto = block_sum(Pair{back > 0 ? (int64_t(1) << 32) | back : 0, r.more}, sh_pair, &all);
+    const Pair upto = block_sum(Pair{back > 0 ? (int64_t(1) << 32) | back : 0, r.more}, min(kChunk, p.batch - b0), sh_pair, &all);
     end = tokens + upto.y;
     if (p.batch > kChunk) tokens = 0;        // summed up again below
     else tokens = all.y;
@@ -227,15 +225,18 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
   for (int b0 = 0; b0 < p.batch; b0 += kChunk) {
     const int b = b0 + tid;
     int64_t all;
+    const int n = min(kChunk, p.batch - b0);
     if (p.batch > kChunk) {
+      __syncthreads();                       // sh has been read
       r = row(b, false);
-      end = tokens + block_sum(r.more, sh, &all);
+      end = tokens + block_sum(r.more, n, sh, &all);
       tokens += all;
+      __syncthreads();
     }
     int64_t need = 0;
     const bool fits = b < p.batch && !r.ends && r.len + r.more <= row_tokens && end <= p.max_tokens;
     if (fits) need = pages_of(r.len + r.more, p) - pages_of(r.len, p);
-    const int64_t upto = wanted + block_sum(need, sh, &all);
+    const int64_t upto = wanted + block_sum(need, n, sh, &all);
     wanted += all;
     const bool ok = fits && (need == 0 || upto <= total);
     if (b < p.batch) {
