@@ -341,7 +341,7 @@ cudaError_t launch_pages_update(const PagesUpdate& u, cudaStream_t st) {
   p.plan = p.inline_tokens ? nullptr : reinterpret_cast<plan::Request*>(static_cast<uint8_t*>(u.ws) + 16);
   p.err = device_error_word();
   const cudaError_t e = launch_pdl(plan::k_pages_plan, dim3(1), dim3(plan::kChunk), 0, st, p);
-  if (e != cudaSuccess || p.inline_tokens) return e;
+  if (e != cudaSuccess || p.inline_tokens || u.max_tokens == 0) return e;
   const int64_t per_block = plan::kSpreadThreads * plan::kSpreadTokens;
   const int blocks = (int)((u.max_tokens + per_block - 1) / per_block);
   return launch_pdl(plan::k_pages_spread, dim3(blocks), dim3(plan::kSpreadThreads), 0, st, p);

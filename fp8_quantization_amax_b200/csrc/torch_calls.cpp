@@ -79,12 +79,15 @@ double real(PyObject* o) {
   return v;
 }
 
-// Every tensor of a call lies on one CUDA device.
+// The CUDA device on which every tensor of a call lies; current while this lives.
 struct Device {
-  int64_t index;
-  Device(const at::Tensor& t, const char* name) : index(t.is_cuda() ? t.get_device() : -1) {
-    if (index < 0) wrong_value(std::string(name) + " must be a CUDA tensor (this library has no CPU path)");
+  c10::DeviceIndex index;
+  c10::cuda::CUDAGuard guard;
+  static c10::DeviceIndex of(const at::Tensor& t, const char* name) {
+    if (!t.is_cuda()) wrong_value(std::string(name) + " must be a CUDA tensor (this library has no CPU path)");
+    return (c10::DeviceIndex)t.get_device();
   }
+  Device(const at::Tensor& t, const char* name) : index(of(t, name)), guard(index) {}
   void holds(std::initializer_list<const at::Tensor*> all) const {
     for (const at::Tensor* t : all)
       if (t && !(t->is_cuda() && t->get_device() == index))
@@ -148,7 +151,7 @@ struct Workspace {
       p = t.data_ptr();
       bytes = t.nbytes();
     } else if (need > 0) {
-      own = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)dev.index));
+      own = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev.index));
       p = own.data_ptr();
       bytes = need;
     }
@@ -156,20 +159,17 @@ struct Workspace {
 };
 
 at::Tensor made(const Device& dev, at::ScalarType type, at::IntArrayRef shape) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev.index));
+  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev.index));
 }
 
-// Run `call(stream)` with the device current, on its current stream.
+// Run `call(stream)` on the device's current stream.
 template <class F>
 void launch(const Device& dev, const char* fn, const F& call) {
   fp8q_status st;
-  {
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
-    fp8q_stream_t stream = (fp8q_stream_t)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
-    Py_BEGIN_ALLOW_THREADS
-    st = call(stream);
-    Py_END_ALLOW_THREADS
-  }
+  fp8q_stream_t stream = (fp8q_stream_t)c10::cuda::getCurrentCUDAStream(dev.index).stream();
+  Py_BEGIN_ALLOW_THREADS
+  st = call(stream);
+  Py_END_ALLOW_THREADS
   if (st != FP8Q_OK) {
     PyObject* e = PyObject_CallFunction(g_error, "si", fn, (int)st);
     if (e) {

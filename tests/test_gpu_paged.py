@@ -236,6 +236,30 @@ def test_attention_outputs_given_strided_and_wide_table():
     assert (room[:, :16] == 7.0).all()
 
 
+def test_attention_without_pages_or_cache():
+    """No table column: nothing is visible.  A cache of no pages: every visible token is reported, and
+    counts as zeros."""
+    q = dev_bf16(bf16(np.random.default_rng(1), 3, 8, 64))
+    s = torch.ones(2, device="cuda")
+    lens = torch.tensor([5, 0, 70], dtype=torch.int32, device="cuda")
+    k = torch.zeros((2, 16, 2, 64), dtype=torch.uint8, device="cuda")
+    out, lse = fq.fp8_attention_paged(q, k, k, s, s, torch.empty((3, 0), dtype=torch.int32, device="cuda"), lens)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and torch.isneginf(lse).all() and fq.device_status() == 0
+    none = k[:0]
+    out, lse = fq.fp8_attention_paged(q, none, none, s, s, torch.zeros((3, 5), dtype=torch.int32, device="cuda"), lens)
+    torch.cuda.synchronize()
+    assert fq.device_status() == 4
+    assert (out == 0).all() and np.allclose(host(lse)[[0, 2]], np.log([[5.0], [70.0]]), rtol=1e-6)
+
+
+@pytest.mark.parametrize("lens", [[64], [63], [17, 1], [1, 16, 2], [32, 32], [33] * 9, [65, 3, 64], [5] * 40 + [200]])
+@pytest.mark.parametrize("heads", [1, 8])
+def test_attention_few_tiles(lens, heads):
+    """Around the number of tiles from which a request is divided, with one head's tiles on all warps or few."""
+    attend(sum(lens), lens, heads, 4, 64, 16, 0, 1, max_pages=max(-(-n // 16) for n in lens))
+
+
 def test_attention_same_bits_again_and_beside_other_work():
     rng = np.random.default_rng(11)
     c = Cache(rng, [5000, 300, 7000], 8, 128, 16, 0, 1)
@@ -458,6 +482,41 @@ def test_append_many_tokens_and_layouts():
     append_case(3, 300, 8, 8, 128, 1, 0, 3, 128, False, False, layout="htd")
 
 
+def test_append_rows_aligned_to_eight_bytes():
+    rng = np.random.default_rng(12)
+    T, hq, hk, d = 50, 4, 2, 128
+    kv = torch.zeros((4, 16, hk, d), dtype=torch.uint8, device="cuda")
+    qkv = dev_bf16(bf16(rng, T, hq + 2 * hk, d))
+    room = torch.zeros(T * ((hq + 2 * hk) * d + 4) + 4, dtype=torch.bfloat16, device="cuda")
+    odd = room[4:].as_strided((T, hq + 2 * hk, d), ((hq + 2 * hk) * d + 4, d, 1))
+    odd.copy_(qkv)
+    turns, slots = fq.rope_turns(d, device="cuda")[0], torch.randperm(64, device="cuda")[:T]
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    got = []
+    for x in (qkv, odd):
+        k, v = kv.clone(), kv.clone()
+        ks, vs = torch.zeros((hk, 64), device="cuda"), torch.zeros((hk, 64), device="cuda")
+        out = fq.fp8_kv_append(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], slots, k, v, ks, vs, 0, 3, positions=pos, turns=turns)
+        got.append((out.clone(), k, v, ks, vs))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("T", [16 * 592, 16 * 592 + 1, 3 * 592 - 1, 593])
+def test_append_blocks_of_all_sizes(T):
+    """Token counts around whole waves of blocks: every token's row is the quantizer's."""
+    rng = np.random.default_rng(T)
+    x = bf16(rng, T, 1, 128)
+    P = -(-T // 16)
+    k = torch.zeros((P, 16, 1, 128), dtype=torch.uint8, device="cuda")
+    v, s1, s2 = k.clone(), torch.zeros((1, P * 16), device="cuda"), torch.zeros((1, P * 16), device="cuda")
+    fq.fp8_kv_append(None, dev_bf16(x), dev_bf16(x), torch.arange(T, device="cuda"), k, v, s1, s2, 0, 3)
+    c, s = fq.fp8_quantize(dev_bf16(x).view(T, 128), 0, fq.GROUP_1x128)
+    torch.cuda.synchronize()
+    assert torch.equal(k.view(-1, 128)[:T], c) and torch.equal(k, v)
+    assert torch.equal(s1[0, :T], s.view(-1)) and torch.equal(s1, s2)
+
+
 def test_append_in_place_equals_apart():
     a = append_case(4, 100, 8, 2, 128, 16, 0, 3, 128, False, True, inplace=True)
     b = append_case(4, 100, 8, 2, 128, 16, 0, 3, 128, False, True)
@@ -630,6 +689,19 @@ def test_pages_nothing_and_empty():
                                  free, count, 16, 0)
     torch.cuda.synchronize()
     assert host(got[3]).tolist() == [1] and int(host(lens)[0]) == 7
+
+
+def test_pages_many_requests_without_tokens():
+    B = 1500
+    free, count = torch.arange(2000, dtype=torch.int32, device="cuda"), torch.tensor([500], dtype=torch.int32, device="cuda")
+    table = torch.arange(500, 2000, dtype=torch.int32, device="cuda").view(B, 1)
+    lens, added = torch.full((B,), 3, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    added[7::100] = -1
+    got = fq.fp8_kv_pages_update(table, lens, added, free, count, 16, 0)
+    torch.cuda.synchronize()
+    assert got[0].numel() == 0 and int(host(count)[0]) == 515
+    assert host(free)[500:515].tolist() == list(range(507, 2000, 100))
+    assert host(lens).tolist() == [0 if b % 100 == 7 else 3 for b in range(B)]
 
 
 def test_pages_bad_counts_are_clipped_and_reported():
