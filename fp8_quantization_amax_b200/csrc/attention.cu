@@ -10,8 +10,8 @@
 // group of 8 every byte meets 8 multiply-adds, 52 T a second at the memory's rate, above the fp32
 // pipes' 36 T: the products go to the tensor cores, m16n8k16 with f16 operands and fp32 sums.
 // Every code is exact in f16, a query (bf16) times a power of two of its row is as well, and only
-// the softmax weights are rounded to f16 (half a step is 2^-12 of a weight, below the output's
-// bf16 2^-9).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
+// the softmax weights are rounded to f16 (half a step is 2^-11 of a weight, below the output's
+// bf16 2^-8).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
 //
 //   S^T (token x query): A = K (rows: 16 tokens), B = q (columns: 8 query heads)
 //   O^T (dim x query):   A = V^T (rows: 16 dims),  B = P^T (columns: 8 query heads)
@@ -32,8 +32,19 @@
 //
 // All requests' tiles laid end to end, with what a change of request costs, are divided evenly over
 // one wave of blocks (kv_pages.cuh), from the lengths on the device: ragged batches and one long
-// request fill the machine alike.  A request whose tiles are shared leaves fp32 partial results, joined by a second launch in the
-// blocks' order, so results do not depend on timing.
+// request fill the machine alike.  A request whose tiles are shared leaves fp32 partial results,
+// joined by a second launch in the blocks' order, so results do not depend on timing.
+//
+// Measured (us a call, calls back to back in a graph; HBM's floor at 6.53 TB/s):
+//   64 requests of 2000 .. 8192 tokens, 64 + 2 * 8 heads of 128    112.5 (102.6: 91 %)
+//   one request of 131072 tokens, a scale per token and head        56.5 (42.4)
+//   16 requests of 130 .. 4096 tokens, 32 + 2 * 8 heads of 128      21.7 (9.3)
+// The first runs at HBM's rate but for the 4 us before its first tile and the last blocks' end (345
+// instructions for 16 tokens of a head, 53 % of the issue slots); the shorter the work, the more its
+// fixed parts show: 4 us to the first tile (lengths, division, table, first copies), 1 us from the last
+// block's end to the second launch, 4 us of that.  Copies of whole tiles by the tensor unit (a box of 16
+// tokens of a head, a barrier a stage) were slower (116 / 62 us): the boxes are small, and what
+// limits the copies is not their instructions.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -49,9 +60,10 @@ namespace attn {
 
 constexpr int kMaxWarps = 16;
 constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 2;                  // least share of a block (1: 11.4 us for 1500 tokens against 10.6; 4: 11.1)
+constexpr int kWholeTiles = 4;                // requests of fewer tiles a warp are not divided (may_share)
 constexpr int64_t kMaxCost = 0x7FFFFFFF;      // of all requests
-constexpr int kTurn = 3;                      // a change of request, in tiles of a phase (see Params::turn)
+constexpr int kTurn = 3;                      // a change of request in tiles of a phase (16 ragged requests: 0 24.9 us, 1 23.2, 2 22.2, 3 21.6, 4 21.8)
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
@@ -299,8 +311,9 @@ __device__ __forceinline__ int swizzled(int row, int c) {
 template <int DP>
 constexpr int kStageBytes = 2 * kAttnTile * DP + 2 * kAttnTile * 4;
 
-// One block per SM.  Up to 128 registers a thread 16 warps share an SM; two row tiles of 128 dims or
-// one of 256 need more, and 8 warps.
+// One block per SM.  Up to 128 registers a thread 16 warps share an SM (8 warps at the same shapes: 117
+// against 106 us for 64 requests of up to 8192 tokens, 24.4 against 25.0 for 16 of up to 4096); two row
+// tiles of 128 dims or one of 256 need more, and 8 warps.
 __host__ __device__ constexpr int warps_of(int dp, int nh) { return dp * nh <= 128 ? 16 : 8; }
 // as many stages as fit next to one another in about 200 KB, at most 6
 __host__ __device__ constexpr int stages_of(int dp, int nh) {
@@ -344,7 +357,7 @@ __device__ __forceinline__ void enter(const Params& p, Cursor& c, int first) {
   c.n = clamped_len(p, c.b);
   c.tiles = attn_range(c.n, p.window, p.sinks).tiles;
   c.first = first;
-  c.end = min(c.tiles, first + c.left);
+  c.end = p.part ? min(c.tiles, first + c.left) : c.tiles;         // (undivided: see may_share)
 }
 // to the next request with tiles
 __device__ __forceinline__ void advance(const Params& p, Cursor& c) {
@@ -469,7 +482,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   c.b = sh_req;
   c.left = t_end - t_begin;
   enter(p, c, t_begin - sh_base);
-  if (c.first >= c.tiles) advance(p, c);     // the share begins behind the request's last tile
+  // the share begins behind the request's last tile; undivided requests are their first tile's block's
+  if (c.first >= c.tiles || (!p.part && c.first > 0)) advance(p, c);
   load = c;
 
   auto tile_token = [&](int i, int n) {
@@ -948,8 +962,9 @@ struct Shape {
   int64_t image;           // floats of one partial result
 };
 
-// head_dim is padded to 64, 128 or 256.  Groups above 8 query heads use both row halves of the
-// first product (two tiles a warp) where the registers suffice.
+// head_dim is padded to 64, 128 or 256.  Groups above 8 query heads have two tiles of query rows a warp,
+// so a tile's codes are read and decoded once for both, where the registers suffice: 81 against 99 us
+// (64 requests of up to 4096 tokens, 9 query heads a head of 128), 19.8 against 22.2 (16 requests, 16).
 inline Shape shape_of(int heads, int group, int head_dim) {
   Shape s;
   s.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
@@ -987,18 +1002,20 @@ cudaError_t launch_dims(const Params& p, const Shape& s, bool join, cudaStream_t
   return launch<FMT, 256, 1, TOKEN_SCALES>(p, s, join, st);
 }
 
-// Can a request be shared?  Not one of a single tile; and the first share, which a lone request begins
-// in, is at least kMinTiles
-inline bool may_share(int64_t batch, int64_t max_tokens) {
-  return (max_tokens + kAttnTile - 1) / kAttnTile > (batch == 1 ? kMinTiles : 1);
+// Are requests divided over blocks?  Where they cannot have more than kWholeTiles tiles a warp, each stays
+// with the block in whose share it begins, and there is no second launch.  us whole / divided: one request
+// of 33 tokens (2 tiles a warp) 6.8 / 8.8, of 100 (4 a warp) 9.4 / 9.9, 300 of up to 100 21.2 / 24.2, but
+// one of 160 (5 a warp) 10.4 / 9.5.
+inline bool may_share(const Shape& s, int64_t max_tokens) {
+  return (max_tokens + kAttnTile - 1) / kAttnTile > kWholeTiles * s.phases;
 }
 
 }  // namespace attn
 
 // Walks every worker's share with the kernel's own functions, for several costs of a change of
 // request: each tile of each request is held once, a worker holds parts of at most two shared
-// requests (the first and the last of its share), the workers named by a shared request's descriptor
-// are those that hold its tiles, and none is shared where the host plans no second launch.
+// requests (the first and the last of its share), and the workers named by a shared request's
+// descriptor are those that hold its tiles.
 static int check_split(const int* lens, int64_t batch, int window, int sinks, int most, int turn) {
   int64_t total = 0;
   for (int64_t b = 0; b < batch; ++b) total += attn_cost(attn_range(lens[b], window, sinks).tiles, turn);
@@ -1034,7 +1051,6 @@ static int check_split(const int* lens, int64_t batch, int window, int sinks, in
       if (w > first && !at_begin) return 10;
     }
     if (held != n) return 11;
-    if (first != last && !attn::may_share(batch, (int64_t)n * kAttnTile)) return 12;
     base += attn_cost(n, turn);
   }
   return 0;
@@ -1060,9 +1076,9 @@ int check_attention_split(const int* lens, int64_t batch, int window, int sinks,
   return 0;
 }
 
-size_t attention_workspace_bytes(int64_t batch, int64_t max_tokens, int heads, int group, int head_dim) {
-  if (!attn::may_share(batch, max_tokens)) return 0;
+size_t attention_workspace_bytes(int64_t max_tokens, int heads, int group, int head_dim) {
   const attn::Shape s = attn::shape_of(heads, group, head_dim);
+  if (!attn::may_share(s, max_tokens)) return 0;
   return (size_t)s.workers * 16 + 256 + (size_t)2 * s.workers * s.vheads * s.image * 4;
 }
 
@@ -1092,7 +1108,7 @@ cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q,
   p.phases = s.phases;
   p.turn = attn::kTurn * s.phases;
   p.workers = s.workers;
-  const bool join = attn::may_share(batch, max_pages * c.page_size);
+  const bool join = attn::may_share(s, max_pages * c.page_size);
   p.desc = join ? static_cast<int4*>(ws) : nullptr;
   p.part = join ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)s.workers * 16 + 255) / 256 * 256) : nullptr;
   p.err = device_error_word();

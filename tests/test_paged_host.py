@@ -74,8 +74,8 @@ def test_bad_caches_are_refused(L, change, status):
     (dict(table=None), 1), (dict(table=MIS4), 1), (dict(q_stride=508), 1), (dict(out_stride=500), 1), (dict(q_stride=256), 1),
     (dict(q_heads=0), 1), (dict(q_heads=7), 1), (dict(batch=-1), 1), (dict(max_pages=-1), 1), (dict(window=-1), 1),
     (dict(sinks=-1), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1),
-    (dict(lse=MIS4), 1), (dict(max_pages=1 << 28), 2), (dict(batch=1 << 12, max_pages=1 << 19), 2), (dict(q_heads=1 << 17), 2), (dict(ws=None, ws_bytes=0), 3),
-    (dict(ws_bytes=100), 3), (dict(ws=MIS), 3), (dict(batch=0, q=None, out=None), 0),
+    (dict(lse=MIS4), 1), (dict(max_pages=1 << 28), 2), (dict(batch=1 << 12, max_pages=1 << 19), 2), (dict(q_heads=1 << 17), 2), (dict(max_pages=500, ws=None, ws_bytes=0), 3),
+    (dict(max_pages=500, ws_bytes=100), 3), (dict(max_pages=500, ws=MIS), 3), (dict(batch=0, q=None, out=None), 0),
 ])
 def test_attention_refuses(L, change, status):
     assert L.fp8_attention_paged(*attention_args(pages(), **change)) == status
@@ -115,8 +115,9 @@ def test_workspace_sizes(L):
     assert fq.pages_workspace_bytes(1024, 4096) == 0
     assert fq.pages_workspace_bytes(1024, 4097) >= 1024 * 8
     assert fq.pages_workspace_bytes(-1, 5) == 0
-    assert fq.attention_workspace_bytes(1, 64, 32, 8, 128) == 0            # one block holds all there can be
-    assert fq.attention_workspace_bytes(1, 65, 32, 8, 128) > 0
+    for batch in (1, 9):                                                   # short requests are not divided
+        assert fq.attention_workspace_bytes(batch, 64, 32, 8, 128) == 0
+        assert fq.attention_workspace_bytes(batch, 1040, 32, 8, 128) > 0
     assert fq.attention_workspace_bytes(1, 4096, 30, 8, 128) == 0          # not a layout
     a = fq.attention_workspace_bytes(1, 4096, 32, 8, 128)
     assert a == fq.attention_workspace_bytes(64, 1 << 20, 32, 8, 128)      # set by the machine, not the lengths
@@ -223,6 +224,11 @@ def test_attention_split_holds_for_any_batch():
         lens = [rng.choice((0, 1, 15, 16, 17, rng.randint(0, 3000))) for _ in range(rng.randint(1, 40))]
         for window, sinks in ((0, 0), (1, 0), (1, 1), (rng.randint(1, 600), rng.randint(0, 50)), (100, 10 ** 6)):
             assert fq.check_attention_split(lens, window, sinks, rng.choice((1, 2, 37, 148, 296, 1184))) == 0
+    for workers in (1, 2, 3, 37, 148, 1024):
+        for n in range(0, 200):
+            assert fq.check_attention_split([n], 0, 0, workers) == 0
+            assert fq.check_attention_split([n, 16, n], 0, 0, workers) == 0
+            assert fq.check_attention_split([n % 17] * 40, 0, 0, workers) == 0
     assert fq.check_attention_split([], 0, 0, 148) == 0
     assert fq.check_attention_split([131072], 0, 0, 296) == 0
     assert fq.check_attention_split([1], -1, 0, 148) == -1
