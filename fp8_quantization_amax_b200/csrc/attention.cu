@@ -473,7 +473,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   }
   const uint8_t* kbase = p.c.k + (int64_t)kvh * p.c.head_stride;
   const uint8_t* vbase = p.c.v + (int64_t)kvh * p.c.head_stride;
-  const bool tile_in_page = p.c.page_size % kAttnTile == 0;
+  // tokens of a block that lies in one page: 16, 8, or 0 where pages do not divide into such
+  const int sub = p.c.page_size % 16 == 0 ? 16 : p.c.page_size % 8 == 0 ? 8 : 0;
   const int row0 = lane / DPC, piece = lane % DPC;                 // this lane's first row and its piece in a copy
   const bool has_piece = 16 * piece < D;
   const uint32_t token16 = (uint32_t)(p.c.token_stride / 16), page16 = (uint32_t)(p.c.page_stride / 16);
@@ -503,14 +504,10 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + r0) * D) + lane * 128);
   };
 
-  // ---- copies: `i_load` is the next tile to copy.  Where a tile lies in one page, lane l holds the
-  // page of the l-th of the warp's 32 tiles from i_load - used * phases on, else `pages` is the page of
-  // this lane's token (lane % 16) of the next tile; -1 where there is none
-  int i_load = load.first + phase, pages = -1, used = 32;
-  auto page_at = [&](int i, int tok) {
-    return i < load.end && tok < load.n
-               ? __ldg(p.table + (int64_t)load.b * p.max_pages + div_u32((uint32_t)tok, p.c.page_div)) : -1;
-  };
+  // ---- copies: `i_load` is the next tile to copy.  Where pages divide into blocks of `sub` tokens, lane l
+  // holds the page of the l-th block from the tile i_load - used on, and its place in the page; else
+  // those of this lane's token (lane % 16) of the next tile.  -1 where there is none
+  int i_load = load.first + phase, pages = -1, offs = 0, used = 32;
   auto find_pages = [&]() {
     while (i_load >= load.end && load.b < p.batch) {
       advance(p, load);
@@ -518,29 +515,44 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       used = 32;
       if (load.b < p.batch) prefetch_q(load.b);
     }
-    if (load.b >= p.batch) return;
-    if (!tile_in_page) {
-      pages = page_at(i_load, tile_token(i_load, load.n) + (lane & 15));
-    } else if (used == 32) {
-      // (a place past the request's last tile may be beyond the tokens' range: page_at does not read it)
-      const int i = i_load + lane * p.phases;
-      pages = page_at(i, i < load.end ? tile_token(i, load.n) : 0);
-      used = 0;
+    if (load.b >= p.batch || (sub > 0 && used < 32)) return;
+    int i = i_load, tok = lane & 15;
+    if (sub == 16) i += lane * p.phases, tok = 0;
+    if (sub == 8) i += (lane >> 1) * p.phases, tok = 8 * (lane & 1);
+    pages = -1;
+    if (i < load.end) {                      // (a place past the request's last tile may leave the tokens' range)
+      tok += tile_token(i, load.n);
+      const uint32_t col = div_u32((uint32_t)tok, p.c.page_div);
+      offs = tok - (int)(col * (uint32_t)p.c.page_size);
+      if (tok < load.n) pages = __ldg(p.table + (int64_t)load.b * p.max_pages + col);
     }
+    used = 0;
   };
   auto issue = [&](int slot_index) {
     if (load.b < p.batch) {
       const uint32_t dst = ring_u + slot_index * kBytes;
       const int tok_load = tile_token(i_load, load.n);
-      const bool whole = all_visible(tok_load, load.n);
-      const int page = tile_in_page ? __shfl_sync(0xFFFFFFFFu, pages, used) : pages;
-      if (tile_in_page && whole && (uint32_t)page < (uint32_t)p.c.num_pages) {
-        const int off = tok_load - (int)(div_u32((uint32_t)tok_load, p.c.page_div) * (uint32_t)p.c.page_size);
+      bool whole = sub > 0 && all_visible(tok_load, load.n);
+      int page = pages, off = offs, page8 = 0, off8 = 0;           // of the tile's tokens 0 .. 7 or 15, and of 8 .. 15
+      if (sub > 0) {
+        page = __shfl_sync(0xFFFFFFFFu, pages, used);
+        off = __shfl_sync(0xFFFFFFFFu, offs, used++);
+        page8 = page;
+        off8 = off + 8;
+        if (sub == 8) {
+          page8 = __shfl_sync(0xFFFFFFFFu, pages, used);
+          off8 = __shfl_sync(0xFFFFFFFFu, offs, used++);
+        }
+        whole = whole && (uint32_t)page < (uint32_t)p.c.num_pages && (uint32_t)page8 < (uint32_t)p.c.num_pages;
+      }
+      if (whole) {
         if (has_piece) {
           // places in units of 16 bytes fit 32 bits (checked on the host)
           uint32_t at = (uint32_t)page * page16 + (uint32_t)(off + row0) * token16 + piece;
+          const uint32_t at8 = (uint32_t)page8 * page16 + (uint32_t)(off8 + row0) * token16 + piece;
 #pragma unroll
           for (int k = 0; k < kAttnTile / RPI; ++k) {
+            if (k * RPI == 8) at = at8;
             const uint32_t to = dst + row0 * DP + 16 * swizzled<DP>(k * RPI + row0, piece) + k * RPI * DP;
             cp_async16(to, kbase + (uint64_t)at * 16);
             cp_async16(to + kAttnTile * DP, vbase + (uint64_t)at * 16);
@@ -548,17 +560,20 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
           }
         }
         if constexpr (TOKEN_SCALES) {
-          const int64_t slot = (int64_t)page * p.c.page_size + off + (lane & 15);
+          const int64_t slot = (int64_t)((lane & 8) ? page8 : page) * p.c.page_size + ((lane & 8) ? off8 : off) + (lane & 7);
           const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
                                                  : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
           cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale);
         }
       } else {
-        const int tok = tok_load + (lane & 15);
+        // this lane's token, lane % 16
+        if (sub > 0) {
+          if (lane & 8) page = page8, off = off8;
+          off += lane & 7;
+        }
         const bool ok = (uint32_t)page < (uint32_t)p.c.num_pages;
-        const bool see = visible(tok, load.n);
+        const bool see = visible(tok_load + (lane & 15), load.n);
         if (!ok && see) raise_device_error(p.err, kErrBadPage);
-        const int off = tok - (int)(div_u32((uint32_t)tok, p.c.page_div) * (uint32_t)p.c.page_size);
         const uint32_t place = (uint32_t)page * page16 + (uint32_t)off * token16;
         const uint32_t seen = __ballot_sync(0xFFFFFFFFu, ok && see);
 #pragma unroll
@@ -582,7 +597,6 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         }
       }
       i_load += p.phases;
-      ++used;
     }
     cp_async_commit();
   };
@@ -971,11 +985,19 @@ inline Shape shape_of(int heads, int group, int head_dim) {
   s.nh = group > 8 && s.dp <= 128 ? 2 : 1;
   s.row_tiles = (group + 8 * s.nh - 1) / (8 * s.nh);
   s.vheads = heads * s.row_tiles;
-  const int warps = warps_of(s.dp, s.nh);
+  const int warps = warps_of(s.dp, s.nh), sms = std::max(1, device_sm_count());
+  // Heads are divided over the fewest groups of blocks; over more where that keeps a tenth more warps of
+  // the machine at work (5 of 8 warps with 5 heads of two row tiles, all of them with one head a block)
   s.groups = (s.vheads + warps - 1) / warps;
+  auto busy = [&](int groups) {              // warps at work, on average, of all SMs
+    const int heads = (s.vheads + groups - 1) / groups;
+    return (double)s.vheads * (warps / heads) * std::max(1, sms / groups);
+  };
+  for (int g = s.groups + 1; g <= std::min(s.vheads, 16); ++g)
+    if (busy(g) > 1.1 * busy(s.groups)) s.groups = g;
   s.heads_per_block = (s.vheads + s.groups - 1) / s.groups;
   s.phases = warps / s.heads_per_block;
-  s.workers = std::min(kMaxWorkers, std::max(1, device_sm_count() / s.groups));
+  s.workers = std::min(kMaxWorkers, std::max(1, sms / s.groups));
   s.image = s.nh * (8 * s.dp + 16);
   return s;
 }

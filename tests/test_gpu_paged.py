@@ -165,6 +165,15 @@ def test_attention_one_head_shared_by_warps():
     attend(3, [3000, 40, 700], 1, 2, 256, 32, 1, 0)
 
 
+@pytest.mark.parametrize("heads,group,d", [(5, 12, 128), (10, 4, 128), (3, 16, 128), (17, 1, 64), (1, 16, 256), (5, 9, 192),
+                                           (9, 12, 256), (2, 40, 160)])
+@pytest.mark.parametrize("size", [8, 16, 24])
+def test_attention_groups_of_heads(heads, group, d, size):
+    """Heads that do not fill a block's warps, wide heads with many query heads; pages of whole and half tiles."""
+    attend(heads + d, [70, 1, 333, 16, 0, 1200], heads, group, d, size, 0, 1)
+    attend(heads + d, [64, 200], heads, group, d, size, 1, 3)
+
+
 def test_attention_scale_and_extreme_scores():
     """Scores far apart (one token takes all), tiny and huge queries, scales many octaves apart."""
     rng = np.random.default_rng(5)
