@@ -131,6 +131,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
@@ -315,9 +318,13 @@ constexpr int kStageBytes = 2 * kAttnTile * DP + 2 * kAttnTile * 4;
 // against 106 us for 64 requests of up to 8192 tokens, 24.4 against 25.0 for 16 of up to 4096); two row
 // tiles of 128 dims or one of 256 need more, and 8 warps.
 __host__ __device__ constexpr int warps_of(int dp, int nh) { return dp * nh <= 128 ? 16 : 8; }
-// as many stages as fit next to one another in about 200 KB, at most 6
+// Two row tiles of 256 dims leave no registers for the query fragments: they lie in shared memory, each
+// thread's own, beside two stages.  Else as many stages as fit in about 200 KB, at most 6
+__host__ __device__ constexpr bool shared_q(int dp, int nh) { return dp * nh > 256; }
+__host__ __device__ constexpr int query_bytes(int dp, int nh) { return shared_q(dp, nh) ? 16 * nh * dp : 0; }   // of a warp
 __host__ __device__ constexpr int stages_of(int dp, int nh) {
-  return 204800 / (warps_of(dp, nh) * (2 * kAttnTile * dp + 2 * kAttnTile * 4)) < 6
+  return shared_q(dp, nh) ? 2
+         : 204800 / (warps_of(dp, nh) * (2 * kAttnTile * dp + 2 * kAttnTile * 4)) < 6
              ? 204800 / (warps_of(dp, nh) * (2 * kAttnTile * dp + 2 * kAttnTile * 4)) : 6;
 }
 
@@ -457,6 +464,9 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
     }
   }
   const uint32_t ring_u = smem_u32(smem) + (uint32_t)warp * (kStages * kBytes);
+  // this thread's query fragments behind all rings, 16 bytes every 512
+  constexpr bool kSharedQ = shared_q(DP, NH);
+  const uint32_t q_u = smem_u32(smem) + (blockDim.x >> 5) * (kStages * kBytes) + (uint32_t)warp * query_bytes(DP, NH) + 16 * lane;
   if (D < DP) {
     // the pieces past head_dim stay zero: no copy writes them
     for (int i = lane; i < kStages * kBytes / 16; i += 32)
@@ -652,9 +662,14 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       qmul[h][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
       qmul[h][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
 #pragma unroll
-      for (int j = 0; j < DP / 64; ++j)
+      for (int j = 0; j < DP / 64; ++j) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) qb[h][j][i] = pack_f16(bf16_lo(qb[h][j][i]) * f, bf16_hi(qb[h][j][i]) * f);
+        if constexpr (kSharedQ) {
+          sts128(q_u + ((h * (DP / 64) + j) * 2) * 512, qb[h][j][0], qb[h][j][1], qb[h][j][2], qb[h][j][3]);
+          sts128(q_u + ((h * (DP / 64) + j) * 2 + 1) * 512, qb[h][j][4], qb[h][j][5], qb[h][j][6], qb[h][j][7]);
+        }
+      }
     }
 
     St s;
@@ -676,6 +691,18 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         const uint32_t at = ks + g * DP + 16 * swizzled<DP>(g, t + 4 * d);
         const uint4 x = lds128(at), y = lds128(at + 8 * DP);
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+        uint32_t qd[NH][8];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if constexpr (kSharedQ) {
+            const uint4 q0 = lds128(q_u + ((h * (DP / 64) + d) * 2) * 512), q1 = lds128(q_u + ((h * (DP / 64) + d) * 2 + 1) * 512);
+            qd[h][0] = q0.x, qd[h][1] = q0.y, qd[h][2] = q0.z, qd[h][3] = q0.w;
+            qd[h][4] = q1.x, qd[h][5] = q1.y, qd[h][6] = q1.z, qd[h][7] = q1.w;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) qd[h][k] = qb[h][d][k];
+          }
+        }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
           uint32_t a0, a1, a2, a3;
@@ -683,8 +710,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
           decode4<FMT>(yw[m], a1, a3);
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
-            if (d == 0 && m == 0) mma_f16_first(st[h], a0, a1, a2, a3, qb[h][d][2 * m], qb[h][d][2 * m + 1]);
-            else mma_f16(st[h], a0, a1, a2, a3, qb[h][d][2 * m], qb[h][d][2 * m + 1]);
+            if (d == 0 && m == 0) mma_f16_first(st[h], a0, a1, a2, a3, qd[h][2 * m], qd[h][2 * m + 1]);
+            else mma_f16(st[h], a0, a1, a2, a3, qd[h][2 * m], qd[h][2 * m + 1]);
           }
         }
       }
@@ -977,12 +1004,14 @@ struct Shape {
 };
 
 // head_dim is padded to 64, 128 or 256.  Groups above 8 query heads have two tiles of query rows a warp,
-// so a tile's codes are read and decoded once for both, where the registers suffice: 81 against 99 us
-// (64 requests of up to 4096 tokens, 9 query heads a head of 128), 19.8 against 22.2 (16 requests, 16).
+// so a tile's codes are read and decoded once for both.  us with two tiles / with one: 64 requests of
+// up to 4096 tokens, 9 query heads a head of 128, 81 / 99; 16 requests, 16 a head of 128, 19.8 / 22.2; 64
+// requests, 12 a head of 256, 133 / 184; of one head of 256 in all, 16 a head, 7 requests 27.2 / 26.5 and
+// 64 of up to 16384 tokens 71 / 93.
 inline Shape shape_of(int heads, int group, int head_dim) {
   Shape s;
   s.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-  s.nh = group > 8 && s.dp <= 128 ? 2 : 1;
+  s.nh = group > 8 ? 2 : 1;
   s.row_tiles = (group + 8 * s.nh - 1) / (8 * s.nh);
   s.vheads = heads * s.row_tiles;
   const int warps = warps_of(s.dp, s.nh), sms = std::max(1, device_sm_count());
@@ -1005,7 +1034,7 @@ inline Shape shape_of(int heads, int group, int head_dim) {
 template <int FMT, int DP, int NH, bool TOKEN_SCALES>
 cudaError_t launch(const Params& p, const Shape& s, bool join, cudaStream_t st) {
   const int warps = s.heads_per_block * s.phases;
-  const size_t smem = (size_t)warps * stages_of(DP, NH) * kStageBytes<DP>;
+  const size_t smem = (size_t)warps * (stages_of(DP, NH) * kStageBytes<DP> + query_bytes(DP, NH));
   auto* kernel = k_attention<FMT, DP, NH, TOKEN_SCALES>;
   cudaError_t e = ensure_dynamic_smem((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
@@ -1021,7 +1050,7 @@ cudaError_t launch_dims(const Params& p, const Shape& s, bool join, cudaStream_t
     return s.nh == 1 ? launch<FMT, 64, 1, TOKEN_SCALES>(p, s, join, st) : launch<FMT, 64, 2, TOKEN_SCALES>(p, s, join, st);
   if (s.dp == 128)
     return s.nh == 1 ? launch<FMT, 128, 1, TOKEN_SCALES>(p, s, join, st) : launch<FMT, 128, 2, TOKEN_SCALES>(p, s, join, st);
-  return launch<FMT, 256, 1, TOKEN_SCALES>(p, s, join, st);
+  return s.nh == 1 ? launch<FMT, 256, 1, TOKEN_SCALES>(p, s, join, st) : launch<FMT, 256, 2, TOKEN_SCALES>(p, s, join, st);
 }
 
 // Are requests divided over blocks?  Where they cannot have more than kWholeTiles tiles a warp, each stays
