@@ -61,7 +61,9 @@ namespace attn {
 constexpr int kMaxWarps = 16;
 constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
 constexpr int kMinTiles = 2;                  // least share of a block (1: 11.4 us for 1500 tokens against 10.6; 4: 11.1)
-constexpr int kWholeTiles = 4;                // requests of fewer tiles a warp are not divided (may_share)
+constexpr int kWholeTiles = 4;                // requests of fewer tiles a warp are not divided
+constexpr int kSpreadTiles = 32;              // few requests of so many tiles have their heads spread ...
+constexpr int kSpreadPhases = 8;              // ... with so many warps a head at most
 constexpr int64_t kMaxCost = 0x7FFFFFFF;      // of all requests
 constexpr int kTurn = 3;                      // a change of request in tiles of a phase (16 ragged requests: 0 24.9 us, 1 23.2, 2 22.2, 3 21.6, 4 21.8)
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
@@ -364,7 +366,7 @@ __device__ __forceinline__ void enter(const Params& p, Cursor& c, int first) {
   c.n = clamped_len(p, c.b);
   c.tiles = attn_range(c.n, p.window, p.sinks).tiles;
   c.first = first;
-  c.end = p.part ? min(c.tiles, first + c.left) : c.tiles;         // (undivided: see may_share)
+  c.end = p.part ? min(c.tiles, first + c.left) : c.tiles;         // (undivided: see Shape)
 }
 // to the next request with tiles
 __device__ __forceinline__ void advance(const Params& p, Cursor& c) {
@@ -1001,6 +1003,7 @@ struct Shape {
   int row_tiles, vheads;   // query-row groups per key-value head, pairs in all
   int heads_per_block, phases, groups, workers;
   int64_t image;           // floats of one partial result
+  bool whole;              // requests are not divided over blocks: no second launch, no workspace
 };
 
 // head_dim is padded to 64, 128 or 256.  Groups above 8 query heads have two tiles of query rows a warp,
@@ -1008,7 +1011,7 @@ struct Shape {
 // up to 4096 tokens, 9 query heads a head of 128, 81 / 99; 16 requests, 16 a head of 128, 19.8 / 22.2; 64
 // requests, 12 a head of 256, 133 / 184; of one head of 256 in all, 16 a head, 7 requests 27.2 / 26.5 and
 // 64 of up to 16384 tokens 71 / 93.
-inline Shape shape_of(int heads, int group, int head_dim) {
+inline Shape shape_of(int64_t batch, int64_t max_tokens, int heads, int group, int head_dim) {
   Shape s;
   s.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
   s.nh = group > 8 ? 2 : 1;
@@ -1026,6 +1029,25 @@ inline Shape shape_of(int heads, int group, int head_dim) {
     if (busy(g) > 1.1 * busy(s.groups)) s.groups = g;
   s.heads_per_block = (s.vheads + s.groups - 1) / s.groups;
   s.phases = warps / s.heads_per_block;
+  const int64_t tiles = (max_tokens + kAttnTile - 1) / kAttnTile;
+  // Requests that cannot have more than kWholeTiles tiles a warp stay with the block in whose share they
+  // begin, and there is no second launch.  us whole / divided (8 heads of 128, two warps each): 300 requests
+  // of up to 100 tokens 21.2 / 24.2, but one of 160 (5 tiles a warp) 10.4 / 9.5.
+  s.whole = tiles <= kWholeTiles * s.phases;
+  // Where each request can have blocks of its own for one head or a few, its heads are spread over the
+  // machine and it stays whole up to kSpreadTiles.  us spread / else: one request of 33 tokens 4.9 / 6.8,
+  // of 250 6.9 / 9.7, of 500 8.8 / 9.9, of 1000 12.6 / 10.5; 8 of up to 300 8.5 / 11.5.  With 4 warps a head
+  // at most one of 500 tokens takes 10.7, with 16 9.3.
+  if (tiles <= kSpreadTiles)
+    for (int heads = 1; heads <= s.heads_per_block; ++heads) {
+      const int groups = (s.vheads + heads - 1) / heads;
+      if (batch * groups > sms) continue;
+      s.groups = groups;
+      s.heads_per_block = heads;
+      s.phases = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(warps / heads, kSpreadPhases), tiles));
+      s.whole = true;
+      break;
+    }
   s.workers = std::min(kMaxWorkers, std::max(1, sms / s.groups));
   s.image = s.nh * (8 * s.dp + 16);
   return s;
@@ -1051,14 +1073,6 @@ cudaError_t launch_dims(const Params& p, const Shape& s, bool join, cudaStream_t
   if (s.dp == 128)
     return s.nh == 1 ? launch<FMT, 128, 1, TOKEN_SCALES>(p, s, join, st) : launch<FMT, 128, 2, TOKEN_SCALES>(p, s, join, st);
   return s.nh == 1 ? launch<FMT, 256, 1, TOKEN_SCALES>(p, s, join, st) : launch<FMT, 256, 2, TOKEN_SCALES>(p, s, join, st);
-}
-
-// Are requests divided over blocks?  Where they cannot have more than kWholeTiles tiles a warp, each stays
-// with the block in whose share it begins, and there is no second launch.  us whole / divided: one request
-// of 33 tokens (2 tiles a warp) 6.8 / 8.8, of 100 (4 a warp) 9.4 / 9.9, 300 of up to 100 21.2 / 24.2, but
-// one of 160 (5 a warp) 10.4 / 9.5.
-inline bool may_share(const Shape& s, int64_t max_tokens) {
-  return (max_tokens + kAttnTile - 1) / kAttnTile > kWholeTiles * s.phases;
 }
 
 }  // namespace attn
@@ -1127,9 +1141,9 @@ int check_attention_split(const int* lens, int64_t batch, int window, int sinks,
   return 0;
 }
 
-size_t attention_workspace_bytes(int64_t max_tokens, int heads, int group, int head_dim) {
-  const attn::Shape s = attn::shape_of(heads, group, head_dim);
-  if (!attn::may_share(s, max_tokens)) return 0;
+size_t attention_workspace_bytes(int64_t batch, int64_t max_tokens, int heads, int group, int head_dim) {
+  const attn::Shape s = attn::shape_of(batch, max_tokens, heads, group, head_dim);
+  if (s.whole) return 0;
   return (size_t)s.workers * 16 + 256 + (size_t)2 * s.workers * s.vheads * s.image * 4;
 }
 
@@ -1137,7 +1151,7 @@ cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q,
                                    const int* table, int64_t batch, int64_t max_pages, const int* lens, float scale,
                                    int window, int sinks, uint16_t* out, int64_t out_stride, float* lse, void* ws,
                                    cudaStream_t st) {
-  const attn::Shape s = attn::shape_of(c.heads, group, c.head_dim);
+  const attn::Shape s = attn::shape_of(batch, max_pages * c.page_size, c.heads, group, c.head_dim);
   attn::Params p;
   p.c = c;
   p.q = q;
@@ -1159,7 +1173,7 @@ cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q,
   p.phases = s.phases;
   p.turn = attn::kTurn * s.phases;
   p.workers = s.workers;
-  const bool join = attn::may_share(s, max_pages * c.page_size);
+  const bool join = !s.whole;
   p.desc = join ? static_cast<int4*>(ws) : nullptr;
   p.part = join ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)s.workers * 16 + 255) / 256 * 256) : nullptr;
   p.err = device_error_word();

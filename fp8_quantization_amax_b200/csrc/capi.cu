@@ -623,7 +623,7 @@ size_t fp8q_attention_workspace_bytes(int64_t batch, int64_t max_tokens, int64_t
       q_heads % kv_heads != 0 || head_dim < 1 || head_dim > 256 || batch > kMaxTableTokens ||
       max_tokens > kMaxTableTokens)
     return 0;
-  return fp8q::attention_workspace_bytes(max_tokens, (int)kv_heads, (int)(q_heads / kv_heads), (int)head_dim);
+  return fp8q::attention_workspace_bytes(batch, max_tokens, (int)kv_heads, (int)(q_heads / kv_heads), (int)head_dim);
 }
 
 int fp8q_check_attention_split(const int32_t* lens, int64_t batch, int64_t window, int64_t sinks, int workers) {

@@ -193,7 +193,7 @@ cudaError_t launch_pages_update(const PagesUpdate& u, cudaStream_t st);
 int check_attention_split(const int* lens, int64_t batch, int window, int sinks, int workers);
 
 // attention of one token per request over its pages; ws: attention_workspace_bytes, scratch
-size_t attention_workspace_bytes(int64_t max_tokens, int heads, int group, int head_dim);
+size_t attention_workspace_bytes(int64_t batch, int64_t max_tokens, int heads, int group, int head_dim);
 cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q, int64_t q_stride, int group,
                                    const int* table, int64_t batch, int64_t max_pages, const int* lens, float scale,
                                    int window, int sinks, uint16_t* out, int64_t out_stride, float* lse, void* ws,

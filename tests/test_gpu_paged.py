@@ -269,6 +269,18 @@ def test_attention_few_tiles(lens, heads):
     attend(sum(lens), lens, heads, 4, 64, 16, 0, 1, max_pages=max(-(-n // 16) for n in lens))
 
 
+@pytest.mark.parametrize("batch,heads,most", [(1, 1, 15), (140, 1, 16), (100, 1, 40), (18, 8, 200), (19, 8, 200), (2, 40, 513),
+                                              (1, 8, 512), (5, 3, 300), (149, 1, 30), (1, 200, 100)])
+@pytest.mark.parametrize("gran", [1, 3])
+def test_attention_heads_spread(batch, heads, most, gran):
+    """Few short requests: heads on blocks of their own, blocks of a warp or several, more requests than threads."""
+    rng = np.random.default_rng(batch * heads)
+    lens = [int(x) for x in rng.integers(0, most + 1, batch)]
+    lens[batch // 2] = most
+    attend(most, lens, heads, 3, 64, 16, 0, gran, max_pages=-(-most // 16))
+    attend(most + 1, lens, heads, 2, 128, 24, 1, gran, 9, 2, max_pages=-(-most // 24))
+
+
 def test_attention_same_bits_again_and_beside_other_work():
     rng = np.random.default_rng(11)
     c = Cache(rng, [5000, 300, 7000], 8, 128, 16, 0, 1)
