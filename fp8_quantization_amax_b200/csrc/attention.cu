@@ -38,7 +38,9 @@
 // Measured (us a call, calls back to back in a graph; HBM's floor at 6.53 TB/s):
 //   64 requests of 2000 .. 8192 tokens, 64 + 2 * 8 heads of 128    112.5 (102.6: 91 %)
 //   one request of 131072 tokens, a scale per token and head        56.5 (42.4)
-//   16 requests of 130 .. 4096 tokens, 32 + 2 * 8 heads of 128      21.7 (9.3)
+//   16 requests of 130 .. 4096 tokens, 32 + 2 * 8 heads of 128      21.5 (9.3)
+//   16 requests of up to 500 tokens, the same heads                  8.4 (1.4)
+//   one request of 33 tokens                                         4.5
 // The first runs at HBM's rate but for the 4 us before its first tile and the last blocks' end (345
 // instructions for 16 tokens of a head, 53 % of the issue slots); the shorter the work, the more its
 // fixed parts show: 4 us to the first tile (lengths, division, table, first copies), 1 us from the last
@@ -62,8 +64,8 @@ constexpr int kMaxWarps = 16;
 constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
 constexpr int kMinTiles = 2;                  // least share of a block (1: 11.4 us for 1500 tokens against 10.6; 4: 11.1)
 constexpr int kWholeTiles = 4;                // requests of fewer tiles a warp are not divided
-constexpr int kSpreadTiles = 32;              // few requests of so many tiles have their heads spread ...
-constexpr int kSpreadPhases = 8;              // ... with so many warps a head at most
+constexpr int kSpreadTiles = 48;              // few requests of so many tiles have their heads spread ...
+constexpr int kSpreadPhases = 12;             // ... with so many warps a head at most
 constexpr int64_t kMaxCost = 0x7FFFFFFF;      // of all requests
 constexpr int kTurn = 3;                      // a change of request in tiles of a phase (16 ragged requests: 0 24.9 us, 1 23.2, 2 22.2, 3 21.6, 4 21.8)
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
@@ -411,58 +413,70 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   allow_dependent_launch();
   grid_dependency_wait();
 
-  // ---- the cost of all requests; this block's share of it, and the request it begins in.  With at
-  // most one request a thread one sum over the block gives all.
-  const bool single = p.batch <= (int)blockDim.x;
-  int mine = 0;
-  bool empty = false;
-  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
-    const int n = attn_cost(attn_range(clamped_len(p, b), p.window, p.sinks).tiles, p.turn);
-    mine += n;
-    empty |= n == 0;
-  }
-  int total;
-  bool any_empty;
-  const int upto = block_sum(mine, empty, sh_sum[0], &total, &any_empty);
-  const int workers = attn_workers(total, p.workers, kMinTiles);
   const int w = blockIdx.x;
-  if (blockIdx.y == 0 && threadIdx.x == 0 && p.desc) p.desc[w] = make_int4(-1, 0, 0, 0);
-
-  // requests without a visible token: zeros, and an empty sum
-  if (any_empty) {
-    for (int b = w; b < p.batch; b += p.workers) {
-      if (clamped_len(p, b) > 0) continue;
-      if (active && phase == 0) {
-        for (int r = r0; r < min(p.group, r0 + 8 * NH); ++r) {
-          uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D;
-          if (8 * lane < D) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0, 0, 0, 0);
-          if (p.lse && lane == 0) p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = -INFINITY;
-        }
-      }
+  // a request without a visible token: zeros, and an empty sum
+  auto write_empty = [&](int b) {
+    if (!active || phase > 0) return;
+    for (int r = r0; r < min(p.group, r0 + 8 * NH); ++r) {
+      uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D;
+      if (8 * lane < D) *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(0, 0, 0, 0);
+      if (p.lse && lane == 0) p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = -INFINITY;
     }
-  }
-  if (w >= workers || total == 0) return;
-  const AttnSplit split = attn_split(total, workers);
-  const int t_begin = attn_start(split, w), t_end = attn_start(split, w + 1);
-  if (single) {
-    if (mine > 0 && upto - mine <= t_begin && t_begin < upto) {
-      sh_req = threadIdx.x;
-      sh_base = upto - mine;
+  };
+  int workers = p.workers, t_begin = 0, t_end = 1;
+  AttnSplit split = {0, 0};
+  if (!p.part && p.batch <= p.workers) {
+    // ---- undivided requests, no more than blocks: each has its own
+    if (w >= p.batch) return;
+    if (clamped_len(p, w) == 0) {
+      write_empty(w);
+      return;
     }
+    if (threadIdx.x == 0) sh_req = w, sh_base = 0;
   } else {
-    int before = 0;
-    for (int b0 = 0, turn = 1; b0 < p.batch; b0 += blockDim.x, turn ^= 1) {
-      const int b = b0 + threadIdx.x;
-      const int n = b < p.batch ? attn_cost(attn_range(clamped_len(p, b), p.window, p.sinks).tiles, p.turn) : 0;
-      int all;
-      bool any;
-      const int incl = before + block_sum(n, false, sh_sum[turn], &all, &any);
-      if (n > 0 && incl - n <= t_begin && t_begin < incl) {
-        sh_req = b;
-        sh_base = incl - n;
+    // ---- the cost of all requests; this block's share of it, and the request it begins in.  With at
+    // most one request a thread one sum over the block gives all.
+    const bool single = p.batch <= (int)blockDim.x;
+    int mine = 0;
+    bool empty = false;
+    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) {
+      const int n = attn_cost(attn_range(clamped_len(p, b), p.window, p.sinks).tiles, p.turn);
+      mine += n;
+      empty |= n == 0;
+    }
+    int total;
+    bool any_empty;
+    const int upto = block_sum(mine, empty, sh_sum[0], &total, &any_empty);
+    workers = attn_workers(total, p.workers, kMinTiles);
+    if (blockIdx.y == 0 && threadIdx.x == 0 && p.desc) p.desc[w] = make_int4(-1, 0, 0, 0);
+
+    if (any_empty)
+      for (int b = w; b < p.batch; b += p.workers)
+        if (clamped_len(p, b) == 0) write_empty(b);
+    if (w >= workers || total == 0) return;
+    split = attn_split(total, workers);
+    t_begin = attn_start(split, w);
+    t_end = attn_start(split, w + 1);
+    if (single) {
+      if (mine > 0 && upto - mine <= t_begin && t_begin < upto) {
+        sh_req = threadIdx.x;
+        sh_base = upto - mine;
       }
-      before += all;
-      if (before > t_begin) break;           // the same for every thread
+    } else {
+      int before = 0;
+      for (int b0 = 0, turn = 1; b0 < p.batch; b0 += blockDim.x, turn ^= 1) {
+        const int b = b0 + threadIdx.x;
+        const int n = b < p.batch ? attn_cost(attn_range(clamped_len(p, b), p.window, p.sinks).tiles, p.turn) : 0;
+        int all;
+        bool any;
+        const int incl = before + block_sum(n, false, sh_sum[turn], &all, &any);
+        if (n > 0 && incl - n <= t_begin && t_begin < incl) {
+          sh_req = b;
+          sh_base = incl - n;
+        }
+        before += all;
+        if (before > t_begin) break;           // the same for every thread
+      }
     }
   }
   const uint32_t ring_u = smem_u32(smem) + (uint32_t)warp * (kStages * kBytes);
@@ -1035,16 +1049,18 @@ inline Shape shape_of(int64_t batch, int64_t max_tokens, int heads, int group, i
   // of up to 100 tokens 21.2 / 24.2, but one of 160 (5 tiles a warp) 10.4 / 9.5.
   s.whole = tiles <= kWholeTiles * s.phases;
   // Where each request can have blocks of its own for one head or a few, its heads are spread over the
-  // machine and it stays whole up to kSpreadTiles.  us spread / else: one request of 33 tokens 4.9 / 6.8,
-  // of 250 6.9 / 9.7, of 500 8.8 / 9.9, of 1000 12.6 / 10.5; 8 of up to 300 8.5 / 11.5.  With 4 warps a head
-  // at most one of 500 tokens takes 10.7, with 16 9.3.
+  // machine and it stays whole up to kSpreadTiles.  us spread / else, 8 heads of 128: one request of 33
+  // tokens 4.5 / 7.0, of 500 8.3 / 10.1, of 750 9.7 / 10.5, of 1000 11.6 / 10.7; 16 of up to 500 8.4 / 11.8, of up
+  // to 750 9.8 / 12.8; one head of 256, 500 tokens 11.0 / 11.0.  With 8 warps a head at most 16 of up to 500
+  // take 9.5, with 6 10.1.
   if (tiles <= kSpreadTiles)
     for (int heads = 1; heads <= s.heads_per_block; ++heads) {
       const int groups = (s.vheads + heads - 1) / heads;
       if (batch * groups > sms) continue;
       s.groups = groups;
       s.heads_per_block = heads;
-      s.phases = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(warps / heads, kSpreadPhases), tiles));
+      const int64_t most = std::min(warps / heads, kSpreadPhases), rounds = std::max<int64_t>(1, (tiles + most - 1) / most);
+      s.phases = (int)std::max<int64_t>(1, (tiles + rounds - 1) / rounds);     // rounds of even tiles
       s.whole = true;
       break;
     }
