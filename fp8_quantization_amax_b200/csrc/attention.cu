@@ -62,12 +62,14 @@ namespace attn {
 
 constexpr int kMaxWarps = 16;
 constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
-constexpr int kMinTiles = 2;                  // least share of a block (1: 11.4 us for 1500 tokens against 10.6; 4: 11.1)
+// least share of a block, in tiles (1: 11.4 us for one request of 1500 tokens against 10.6; 4: 11.1)
+constexpr int kMinTiles = 2;
 constexpr int kWholeTiles = 4;                // requests of fewer tiles a warp are not divided
 constexpr int kSpreadTiles = 48;              // few requests of so many tiles have their heads spread ...
 constexpr int kSpreadPhases = 12;             // ... with so many warps a head at most
 constexpr int64_t kMaxCost = 0x7FFFFFFF;      // of all requests
-constexpr int kTurn = 3;                      // a change of request in tiles of a phase (16 ragged requests: 0 24.9 us, 1 23.2, 2 22.2, 3 21.6, 4 21.8)
+// a change of request, in tiles of a phase (16 ragged requests: 0 24.9 us, 1 23.2, 2 22.2, 3 21.6, 4 21.8)
+constexpr int kTurn = 3;
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
@@ -287,7 +289,8 @@ __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, in
       if (r >= p.group) continue;
       const float l = s.l[n][e], f = vs * rcp(l);
       if (p.lse && g == 0)
-        p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = l == 0.0f ? -INFINITY : kLn2 * (s.m[n][e] + lg2(l));
+        p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] =
+            l == 0.0f ? -INFINITY : kLn2 * (s.m[n][e] + lg2(l));
       uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D + g * VB;
 #pragma unroll
       for (int c = 0; c < VB / 8; ++c) {
@@ -325,7 +328,8 @@ __host__ __device__ constexpr int warps_of(int dp, int nh) { return dp * nh <= 1
 // Two row tiles of 256 dims leave no registers for the query fragments: they lie in shared memory, each
 // thread's own, beside two stages.  Else as many stages as fit in about 200 KB, at most 6
 __host__ __device__ constexpr bool shared_q(int dp, int nh) { return dp * nh > 256; }
-__host__ __device__ constexpr int query_bytes(int dp, int nh) { return shared_q(dp, nh) ? 16 * nh * dp : 0; }   // of a warp
+// of a warp
+__host__ __device__ constexpr int query_bytes(int dp, int nh) { return shared_q(dp, nh) ? 16 * nh * dp : 0; }
 __host__ __device__ constexpr int stages_of(int dp, int nh) {
   return shared_q(dp, nh) ? 2
          : 204800 / (warps_of(dp, nh) * (2 * kAttnTile * dp + 2 * kAttnTile * 4)) < 6
@@ -482,7 +486,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   const uint32_t ring_u = smem_u32(smem) + (uint32_t)warp * (kStages * kBytes);
   // this thread's query fragments behind all rings, 16 bytes every 512
   constexpr bool kSharedQ = shared_q(DP, NH);
-  const uint32_t q_u = smem_u32(smem) + (blockDim.x >> 5) * (kStages * kBytes) + (uint32_t)warp * query_bytes(DP, NH) + 16 * lane;
+  const uint32_t q_u = smem_u32(smem) + (blockDim.x >> 5) * (kStages * kBytes) + (uint32_t)warp * query_bytes(DP, NH) +
+                       16 * lane;
   if (D < DP) {
     // the pieces past head_dim stay zero: no copy writes them
     for (int i = lane; i < kStages * kBytes / 16; i += 32)
@@ -527,8 +532,13 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   auto prefetch_q = [&](int b) {
     const int bytes = min(8 * NH, p.group - r0) * D * 2;
     if (lane * 128 < bytes)
-      prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + r0) * D) + lane * 128);
+      prefetch_l2(p.q + (int64_t)b * p.q_stride + (int64_t)(kvh * p.group + r0) * D + lane * 64);
   };
+
+  // this lane's scales, of K (lanes 0 .. 15) or V, and a slot's place among them (slots are below 2^31)
+  const float* const scales = (lane < 16 ? p.c.ks : p.c.vs) +
+                              (p.c.gran == 2 ? kvh : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size));
+  auto scale_at = [&](int slot) { return p.c.gran == 2 ? (int64_t)(slot >> 7) * p.c.heads : (int64_t)slot; };
 
   // ---- copies: `i_load` is the next tile to copy.  Where pages divide into blocks of `sub` tokens, lane l
   // holds the page of the l-th block from the tile i_load - used on, and its place in the page; else
@@ -586,10 +596,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
           }
         }
         if constexpr (TOKEN_SCALES) {
-          const int64_t slot = (int64_t)((lane & 8) ? page8 : page) * p.c.page_size + ((lane & 8) ? off8 : off) + (lane & 7);
-          const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
-                                                 : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
-          cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale);
+          const int slot = ((lane & 8) ? page8 : page) * p.c.page_size + ((lane & 8) ? off8 : off) + (lane & 7);
+          cp_async4(dst + 2 * kAttnTile * DP + 4 * lane, scales + scale_at(slot));
         }
       } else {
         // this lane's token, lane % 16
@@ -616,10 +624,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         }
         if constexpr (TOKEN_SCALES) {
           const bool take = (seen >> (lane & 15)) & 1u;
-          const int64_t slot = take ? (int64_t)page * p.c.page_size + off : 0;
-          const int64_t at_scale = p.c.gran == 2 ? (slot >> 7) * p.c.heads + kvh
-                                                 : (int64_t)kvh * ((int64_t)p.c.num_pages * p.c.page_size) + slot;
-          cp_async4_or_zero(dst + 2 * kAttnTile * DP + 4 * lane, (lane < 16 ? p.c.ks : p.c.vs) + at_scale, take);
+          cp_async4_or_zero(dst + 2 * kAttnTile * DP + 4 * lane,
+                            scales + scale_at(take ? page * p.c.page_size + off : 0), take);
         }
       }
       i_load += p.phases;
@@ -711,7 +717,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           if constexpr (kSharedQ) {
-            const uint4 q0 = lds128(q_u + ((h * (DP / 64) + d) * 2) * 512), q1 = lds128(q_u + ((h * (DP / 64) + d) * 2 + 1) * 512);
+            const uint32_t at_q = q_u + (h * (DP / 64) + d) * 1024;
+            const uint4 q0 = lds128(at_q), q1 = lds128(at_q + 512);
             qd[h][0] = q0.x, qd[h][1] = q0.y, qd[h][2] = q0.z, qd[h][3] = q0.w;
             qd[h][4] = q1.x, qd[h][5] = q1.y, qd[h][6] = q1.z, qd[h][7] = q1.w;
           } else {
@@ -844,7 +851,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         if (phase == 0)
           for (int k = 1; k < p.phases; ++k) {
             const int other = warp + k * p.heads_per_block;
-            s.template add_tile<TOKEN_SCALES>(h, reinterpret_cast<const float*>(smem + ((size_t)other * kStages + sh_free[other]) * kBytes), lane);
+            const uint8_t* from = smem + ((size_t)other * kStages + sh_free[other]) * kBytes;
+            s.template add_tile<TOKEN_SCALES>(h, reinterpret_cast<const float*>(from), lane);
           }
         named_barrier(bar, threads);         // the stages are read before they are written again
       }
@@ -979,7 +987,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
         for (int k = warp + 1; k < warp + (int)wpu; ++k) {
           const float b0 = sh[k][0][lane], b1 = sh[k][1][lane];
           const float a0 = fmaxf(m0, b0), a1 = fmaxf(m1, b1);
-          const float f0 = ex2_diff<TOKEN_SCALES>(m0, a0), f1 = ex2_diff<TOKEN_SCALES>(m1, a1), h0 = ex2_diff<TOKEN_SCALES>(b0, a0), h1 = ex2_diff<TOKEN_SCALES>(b1, a1);
+          const float f0 = ex2_diff<TOKEN_SCALES>(m0, a0), f1 = ex2_diff<TOKEN_SCALES>(m1, a1);
+          const float h0 = ex2_diff<TOKEN_SCALES>(b0, a0), h1 = ex2_diff<TOKEN_SCALES>(b1, a1);
           m0 = a0;
           m1 = a1;
           l0 = l0 * f0 + sh[k][2][lane] * h0;
@@ -1059,7 +1068,8 @@ inline Shape shape_of(int64_t batch, int64_t max_tokens, int heads, int group, i
       if (batch * groups > sms) continue;
       s.groups = groups;
       s.heads_per_block = heads;
-      const int64_t most = std::min(warps / heads, kSpreadPhases), rounds = std::max<int64_t>(1, (tiles + most - 1) / most);
+      const int64_t most = std::min(warps / heads, kSpreadPhases);
+      const int64_t rounds = std::max<int64_t>(1, (tiles + most - 1) / most);
       s.phases = (int)std::max<int64_t>(1, (tiles + rounds - 1) / rounds);     // rounds of even tiles
       s.whole = true;
       break;
@@ -1191,7 +1201,8 @@ cudaError_t launch_attention_paged(const KvPages& c, int fmt, const uint16_t* q,
   p.workers = s.workers;
   const bool join = !s.whole;
   p.desc = join ? static_cast<int4*>(ws) : nullptr;
-  p.part = join ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + ((size_t)s.workers * 16 + 255) / 256 * 256) : nullptr;
+  uint8_t* parts = static_cast<uint8_t*>(ws) + ((size_t)s.workers * 16 + 255) / 256 * 256;
+  p.part = join ? reinterpret_cast<float*>(parts) : nullptr;
   p.err = device_error_word();
   const bool token_scales = c.gran >= 2;
   if (fmt == kE4M3)
