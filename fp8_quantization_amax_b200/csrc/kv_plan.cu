@@ -31,7 +31,7 @@ namespace plan {
 constexpr int kChunk = 1024;
 constexpr int kInlineTokens = 4096;
 constexpr int kSpreadThreads = 256;
-constexpr int kSpreadTokens = 4;             // of a thread
+constexpr int kSpreadTokens = 4;             // of a thread (us for 296 thousand tokens: 2 7.6, 4 7.1, 8 8.6)
 
 struct Request {
   int old_len;     // tokens held before
