@@ -365,13 +365,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append
   for (int i = threadIdx.x; i < 2 * 2 * LPR; i += blockDim.x) {
     const int which = i / (2 * LPR), at = i % (2 * LPR);
     const uint16_t* weight = which == 0 ? p.q_weight : p.k_weight;
-    if (weight && 8 * at < p.c.head_dim) {
+    if (!weight) continue;
+    // chunks past head_dim have zeros: their elements are zero, but times what lies here by chance
+    // (NaN, infinity) they would not be, and a row's scale is taken over all its chunks
+    float4 wa = make_float4(0.0f, 0.0f, 0.0f, 0.0f), wb = wa;
+    if (8 * at < p.c.head_dim) {
       const bool split = 8 * at < p.rot && !NEXT;
       const Chunk w = unpack<NEXT>(__ldg(reinterpret_cast<const uint2*>(weight + (split ? 4 * at : 8 * at))),
                                    __ldg(reinterpret_cast<const uint2*>(weight + (split ? pairs + 4 * at : 8 * at + 4))));
-      *reinterpret_cast<float4*>(&sh.weights[which][0][4 * at]) = make_float4(w.a[0].x, w.a[0].y, w.a[1].x, w.a[1].y);
-      *reinterpret_cast<float4*>(&sh.weights[which][1][4 * at]) = make_float4(w.b[0].x, w.b[0].y, w.b[1].x, w.b[1].y);
+      wa = make_float4(w.a[0].x, w.a[0].y, w.a[1].x, w.a[1].y);
+      wb = make_float4(w.b[0].x, w.b[0].y, w.b[1].x, w.b[1].y);
     }
+    *reinterpret_cast<float4*>(&sh.weights[which][0][4 * at]) = wa;
+    *reinterpret_cast<float4*>(&sh.weights[which][1][4 * at]) = wb;
   }
   if (threadIdx.x < nt) {
     const int64_t slot = __ldg(p.slots + t0 + threadIdx.x);
