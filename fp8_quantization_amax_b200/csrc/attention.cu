@@ -9,9 +9,10 @@
 // What bounds it: the codes, 2 heads head_dim bytes a token, are read once from HBM.  With a
 // group of 8 every byte meets 8 multiply-adds, 52 T a second at the memory's rate, above the fp32
 // pipes' 36 T: the products go to the tensor cores, m16n8k16 with f16 operands and fp32 sums.
-// Every code is exact in f16, a query (bf16) times a power of two of its row is as well, and only
-// the softmax weights are rounded to f16 (half a step is 2^-11 of a weight, below the output's
-// bf16 2^-8).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
+// Every code is exact in f16, and so is a query (bf16) times a power of two of its row, but for elements
+// below 2^-31 of the row's largest (off by at most 2^-39 of that).  The softmax weights are rounded to f16:
+// half a step is 2^-11 of a weight, below the output's bf16 2^-8, and 2^-34 of the row's largest weight where
+// that is more (kLift).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
 //
 //   S^T (token x query): A = K (rows: 16 tokens), B = q (columns: 8 query heads)
 //   O^T (dim x query):   A = V^T (rows: 16 dims),  B = P^T (columns: 8 query heads)
@@ -21,7 +22,7 @@
 // tokens g, g + 8 become the second product's operand by a transposition of 8 x 8 halves (movmatrix).
 // The order of the sum over dims and the dims' order in O^T are free, so thread t reads 16
 // contiguous bytes of a K row per 64 dims, and thread g head_dim / 8 contiguous bytes of a V row.
-// The maximum follows the scores only when one exceeds it by 2^8 (f16 holds weights to 2^16): a
+// The maximum follows the scores only when one exceeds it by 2^6 (f16 holds weights to 2^16): a
 // vote a tile instead of a reduction, and next to no rescaling.
 //
 // Each warp streams the tokens of one key-value head on its own through a private ring of
@@ -74,7 +75,13 @@ constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers s
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
 constexpr int kJoinBatch = 8;                 // parts whose loads are in flight together
-constexpr float kSlack = 8.0f;                // a score may exceed the running maximum by this (base 2)
+// The reference lies kLift (base 2) below the maximum that set it and follows when a score exceeds that
+// maximum by kSlack, so a row's largest weight is 2^kLift .. 2^(kLift + kSlack) (f16 ends at 2^16) and what f16
+// rounds away of small ones is at most 2^-(25 + kLift) of the largest.  With the reference at the maximum, 8192
+// tokens of weight 2^-26 beside one of V = 0 gave 0.  us at slacks 8 / 6 / 4 / 2: window 17.6 17.6 17.9 18.5,
+// one kv head 27.1 26.8 27.4 27.5, the other cases alike.
+constexpr float kLift = 9.0f, kSlack = 6.0f;
+static_assert(kLift + kSlack < 16.0f, "weights fit f16");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -152,7 +159,7 @@ __device__ __forceinline__ float lds32(uint32_t addr) {
 }
 
 // 2^x.  Results below 2^-126 become zero unless FULL: that takes four instructions in place of one.
-// Without scales of single tokens the largest weight of a row is at least 2^-kSlack and what
+// Without scales of single tokens the largest weight of a row is at least 2^kLift and what
 // vanishes does not show; a token's scale joins the reference, so with them all weights may be small.
 template <bool FULL>
 __device__ __forceinline__ float ex2(float x) {
@@ -772,7 +779,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) above |= (TOKEN_SCALES ? st[h][e] + vl[e >> 1] : st[h][e]) > s.m[h][e & 1] + kSlack;
+        for (int e = 0; e < 4; ++e)
+          above |= (TOKEN_SCALES ? st[h][e] + vl[e >> 1] : st[h][e]) > s.m[h][e & 1] + (kLift + kSlack);
       if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -782,7 +790,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
             top[e] = TOKEN_SCALES ? fmaxf(st[h][e] + vl[0], st[h][2 + e] + vl[1]) : fmaxf(st[h][e], st[h][2 + e]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], d));
-            top[e] = fmaxf(top[e], s.m[h][e]);
+            top[e] = fmaxf(top[e] - kLift, s.m[h][e]);
           }
           s.rescale(h, ex2_diff<TOKEN_SCALES>(s.m[h][0], top[0]), ex2_diff<TOKEN_SCALES>(s.m[h][1], top[1]));
           s.m[h][0] = top[0];

@@ -8,8 +8,12 @@ import pytest
 import torch
 
 import fp8_quantization_amax_b200 as fq
-from helpers import dev_bf16
+import paged_reference as ref
+from helpers import dev, dev_bf16, host
 from test_gpu_paged import append_case, bf16
+
+#: the largest weight of a row is at least 2^LIFT when weights are rounded to f16
+LIFT = 9
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +53,56 @@ def test_append_after_nan_in_shared_memory(d, interleaved, monkeypatch):
     monkeypatch.setattr(fq, "fp8_kv_append", after_nan)
     for rot in (0, d // 2 // 8 * 8, d):
         append_case(d + rot, 700, 3, 3, d, 24, 0, 3, rot, interleaved, True)
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("gran", [1, 3])
+@pytest.mark.parametrize("below", [22.0, 24.0, 25.6, 27.0])
+def test_attention_keeps_weights_far_below_the_largest(gran, below):
+    """One token takes nearly all the weight and its V is zero, so the others are the whole result; each
+    request is read by one warp a head.  A weight's error is 2^-11 of it, or 2^-25 where it is subnormal in f16,
+    the row's largest being 2^LIFT at least (the tolerance's second line)."""
+    rng = np.random.default_rng(int(below))
+    B, H, G, D, size, n = torch.cuda.get_device_properties(0).multi_processor_count, 16, 2, 64, 16, 8192
+    P = n // size
+    k = rng.integers(0, 256, (n, H, D)).astype(np.uint8)
+    k[(k & 0x7F) >= 0x78] ^= 0x40                             # moderate codes
+    k[:, :, 0] = 0
+    k[5] = 0
+    k[5, :, 0] = 0x38                                         # 1.0
+    v = rng.integers(0x30, 0x41, (n, H, D)).astype(np.uint8)  # 0.5 .. 2
+    v[5] = 0
+    shape = fq.kv_page_scale_shape(P, size, H, gran)
+    ks = np.full(shape, below * np.log(2.0), np.float32)
+    vs = np.ones(shape, np.float32)
+    if gran == 3:
+        vs = np.exp2(rng.uniform(-2, 2, shape)).astype(np.float32)
+        vs[:, 5] = 1.0
+    x = (rng.standard_normal((H * G, D)) * 2e-5).astype(np.float32)
+    x[:, 0] = 1.0
+    qb = (x.view(np.uint32) >> 16).astype(np.uint16)
+    table = np.broadcast_to(np.arange(P, dtype=np.int32), (B, P))
+    cache = [dev(c.reshape(P, size, H, D)) for c in (k, v)]
+    out, lse = fq.fp8_attention_paged(dev_bf16(np.broadcast_to(qb, (B, H * G, D))), *cache, dev(ks), dev(vs), dev(table),
+                                      dev(np.full(B, n, np.int32)), 0, gran, scale=1.0)
+    torch.cuda.synchronize()
+    val, q = ref.decode_table(0), ref.bf16_to_f64(qb)
+    for h in range(H):
+        slots = np.arange(n)
+        kk = val[k[:, h]] * ref.token_scale(ks, gran, slots, h)[:, None]
+        sv = ref.token_scale(vs, gran, slots, h)
+        z = q[h * G:(h + 1) * G] @ kk.T
+        dz = (np.abs(q[h * G:(h + 1) * G]) @ np.abs(kk.T) * (D + 8) * 2.0 ** -22 + np.abs(z) * 2.0 ** -21).max(1)[:, None]
+        p = np.exp(z - z.max(1, keepdims=True))
+        tot = p.sum(1, keepdims=True)
+        want = p @ (val[v[:, h]] * sv[:, None]) / tot
+        tol = want * (2.0 ** -8 + 2.0 ** -11 + 2 * dz + 2.0 ** -19) \
+            + n * 2.0 ** -25 * 2.0 ** -LIFT * (p * sv).max(1, keepdims=True) / tot * 2.0
+        assert (tol < 0.1 * want).all()                       # a lost tail shows
+        for b in (0, 1, B - 1):
+            got = ref.bf16_to_f64(host(out[b, h * G:(h + 1) * G]))
+            assert (np.abs(got - want) <= tol).all(), (h, b, (np.abs(got - want) / want).max())
+            got = host(lse[b, h * G:(h + 1) * G]).astype(np.float64)
+            lw = np.log(tot[:, 0]) + z.max(1)
+            assert (np.abs(got - lw) <= dz[:, 0] + 2.0 ** -20 * (1 + np.abs(lw))).all()
