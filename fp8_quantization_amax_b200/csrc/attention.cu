@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         for (int k = 0; k < 2; ++k) {
           const float kf = lds32(sc + 4 * (g + 8 * k));
           vf[k] = lds32(sc + 4 * (16 + g + 8 * k));
-          vl[k] = lg2_normal(fmaxf(vf[k], 0x1.0p-60f));
+          vl[k] = lg2_normal(fmaxf(fabsf(vf[k]), 0x1.0p-60f));
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             st[h][2 * k] *= kf;
@@ -774,7 +774,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
             for (int h = 0; h < NH; ++h) st[h][2 * k] = st[h][2 * k + 1] = -INFINITY;
           }
       }
-      // V's scale counts towards the reference, so that a weight times its scale fits f16
+      // The magnitude of V's scale counts towards the reference, so that a weight times its scale fits f16
+      // (one below 2^-60 counts as that: the weight itself, at most 2^75 then, has to fit fp32)
       bool above = false;
 #pragma unroll
       for (int h = 0; h < NH; ++h)

@@ -10,7 +10,7 @@ import torch
 import fp8_quantization_amax_b200 as fq
 import paged_reference as ref
 from helpers import dev, dev_bf16, host
-from test_gpu_paged import append_case, bf16
+from test_gpu_paged import Cache, append_case, bf16
 
 #: the largest weight of a row is at least 2^LIFT when weights are rounded to f16
 LIFT = 9
@@ -106,3 +106,24 @@ def test_attention_keeps_weights_far_below_the_largest(gran, below):
             got = host(lse[b, h * G:(h + 1) * G]).astype(np.float64)
             lw = np.log(tot[:, 0]) + z.max(1)
             assert (np.abs(got - lw) <= dz[:, 0] + 2.0 ** -20 * (1 + np.abs(lw))).all()
+
+
+@pytest.mark.parametrize("gran", [2, 3])
+def test_attention_scales_of_either_sign(gran):
+    """Scales of tokens may be negative, as those of heads: their magnitude is what a weight is brought to."""
+    rng = np.random.default_rng(gran)
+    c = Cache(rng, [300, 0, 77], 2, 64, 16, 0, gran)
+    for s, d in ((c.ks, c.dks), (c.vs, c.dvs)):
+        s *= np.where(rng.random(s.shape) < 0.5, -1.0, 1.0).astype(np.float32)
+        d.copy_(dev(s))
+    qb = bf16(rng, 3, 8, 64)
+    out, lse = c.run(dev_bf16(qb))
+    torch.cuda.synchronize()
+    c.check(qb, out, lse, 0.125)
+    # all of them negative: minus the result of their magnitudes
+    c.dvs.copy_(dev(-np.abs(c.vs)))
+    neg, _ = c.run(dev_bf16(qb))
+    c.dvs.copy_(dev(np.abs(c.vs)))
+    pos, _ = c.run(dev_bf16(qb))
+    torch.cuda.synchronize()
+    assert torch.equal(neg[[0, 2]], -pos[[0, 2]])
