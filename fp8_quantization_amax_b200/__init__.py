@@ -793,7 +793,8 @@ def fp8_kv_pages_update(block_table: torch.Tensor, lens: torch.Tensor, added: to
     too unless lens_out / free_count_out are given.  added int32 [batch]: new tokens of each request,
     negative for one that ends.  -> (slots int64 [max_tokens], positions int32 [max_tokens], offsets
     int32 [batch + 1], served int32 [batch], lens_out, free_count_out); max_tokens, an upper bound of
-    the added tokens known on the host, may be left out when slots is given."""
+    the added tokens known on the host, may be left out when slots is given.  Pages recycled before
+    their request ends must be marked by a negative block_table entry."""
     return (_calls or _load_calls()).update(block_table, lens, added, free_pages, free_count, page_size, max_tokens, slots,
                                             positions, offsets, served, lens_out, free_count_out, ws)
 

@@ -3,7 +3,9 @@
 //
 // Requests that end put their pages on the free list; then the others take the pages their new
 // tokens need from its top.  Both are prefix sums over the requests in order, so the result does
-// not depend on timing.  What bounds it: 12 bytes written a token and a few words a request, a
+// not depend on timing.  Table entries below zero (pages given away before) give nothing back: the
+// entries go on the list as they are, and where such a one was among them a second pass over them with
+// sums puts the pages alone.  What bounds it: 12 bytes written a token and a few words a request, a
 // microsecond of traffic at most: the chain of dependent steps (lengths, two sums, table, slots)
 // and the launches are what a call costs.
 //
@@ -14,7 +16,7 @@
 // searches (two dependent loads for 1024 requests), and its threads search between them.
 //
 // Measured (us a call, back to back in a graph): 256 decoding requests, 8 of which end, 5.9; prompts of 96
-// requests, 295 thousand tokens, 7.3 (the floor of the traffic is 0.6).  One launch against two: 6.5 /
+// requests, 295 thousand tokens, 7.3 to 7.5 (the floor of the traffic is 0.6).  One launch against two: 6.5 /
 // 7.1 at 3100 tokens, 9.0 / 7.0 at 6200.
 #include <cuda_runtime.h>
 
@@ -30,6 +32,7 @@ namespace plan {
 
 constexpr int kChunk = 1024;
 constexpr int kInlineTokens = 4096;
+constexpr int kCopies = 4;                   // pages given back that a thread copies at a time
 constexpr int kSpreadThreads = 256;
 constexpr int kSpreadTokens = 4;             // of a thread (us for 296 thousand tokens: 2 7.6, 4 7.1, 8 8.6)
 
@@ -135,26 +138,52 @@ __device__ __forceinline__ int find_by_warp(const int* first, int n, int x) {
 }
 
 // slot and position of token i of request b, whose first one is `first`, and the table entry where it
-// is the first of a new page
-__device__ __forceinline__ void place_token(const Params& p, int i, int b, int first, const Request& r, int total) {
+// is the first of a new page.  Below zero where that holds no page
+__device__ __forceinline__ int place_token(const Params& p, int i, int b, int first, const Request& r, int total) {
   const int64_t pos = (int64_t)r.old_len + (i - first);
   int64_t slot = -1;
+  int page = 0;
   if (r.from >= 0) {
     const int col = (int)div_u32((uint32_t)pos, p.page_div);
     const int off = (int)(pos - (int64_t)col * p.page_size);
     const int held = pages_of(r.old_len, p);
     int* entry = p.table + (int64_t)b * p.max_pages + col;
-    int page;
     if (col < held) {
       page = *entry;
     } else {
-      page = p.free[total - 1 - r.from - (col - held)];
+      page = max(-1, p.free[total - 1 - r.from - (col - held)]);
       if (off == 0) *entry = page;
     }
-    slot = (int64_t)page * p.page_size + off;
+    slot = page < 0 ? -1 : (int64_t)page * p.page_size + off;
   }
   p.slots[i] = slot;
   p.positions[i] = (int)pos;
+  return page;
+}
+
+// entry i of those that the ending requests give back
+__device__ __forceinline__ int back_page(const int* table, int max_pages, const int* first, const int* ending, int givers,
+                                         int i) {
+  const int k = find(first, 0, givers, i);
+  return table[(int64_t)ending[k] * max_pages + (i - first[k])];
+}
+
+// The pages among the `given` entries, in order, to `list`, what does not fit dropped; how many there are.  By
+// the whole block.  Not inlined: the kernel runs through its code once, and code that it jumps over costs too
+// (256 decoding requests 5.85 us against 5.91, 1000 of which 500 end 127.5 against 129.0)
+__device__ __noinline__ int pages_alone(const int* table, int max_pages, int given, int givers, const int* first,
+                                        const int* ending, int* list, int room, Sums<int64_t>& sh) {
+  int kept = 0;
+  for (uint32_t i0 = 0; i0 < (uint32_t)given; i0 += kChunk) {
+    const uint32_t i = i0 + threadIdx.x;
+    const int page = i < (uint32_t)given ? back_page(table, max_pages, first, ending, givers, (int)i) : -1;
+    int64_t pages;
+    const int at = kept + (int)block_sum<int64_t>(page >= 0 ? 1 : 0, kChunk, sh, &pages) - 1;
+    if (page >= 0 && at < room) list[at] = page;
+    kept += (int)pages;
+    __syncthreads();                         // sh has been read
+  }
+  return kept;
 }
 
 __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
@@ -210,17 +239,27 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
       first[k] = (int)(uint32_t)upto.x - back;
       ending[k] = b0 + tid;
     }
-    int64_t room = (int64_t)p.num_pages - total;
-    if (given > room && tid == 0) raise_device_error(p.err, kErrBadPage);
-    if (given < room) room = given;          // what does not fit on the list is dropped
+    const int64_t room = (int64_t)p.num_pages - total;
+    const uint32_t most = (uint32_t)min((int64_t)given, room);
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < (int)room; i += kChunk) {
-      const int k = find(first, 0, givers, i);
-      p.free[total + i] = p.table[(int64_t)ending[k] * p.max_pages + (i - first[k])];
+    bool marked = false;
+    for (uint32_t i0 = tid; i0 < most; i0 += kCopies * kChunk) {
+      int page[kCopies];                     // in flight together
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) page[c] = i0 + c * kChunk < most ? back_page(p.table, p.max_pages, first, ending, givers, i0 + c * kChunk) : 0;
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) {
+        marked |= page[c] < 0;
+        if (i0 + c * kChunk < most) p.free[total + i0 + c * kChunk] = page[c];
+      }
     }
-    total += room;
-    __syncthreads();
+    if (!__syncthreads_or(marked || (uint32_t)given > most)) {
+      total += given;
+      continue;
+    }
+    const int kept = pages_alone(p.table, p.max_pages, given, givers, first, ending, p.free + total, (int)room, sh);
+    if (kept > room && tid == 0) raise_device_error(p.err, kErrBadPage);
+    total += min((int64_t)kept, room);
   }
   __syncthreads();                           // the list is complete
 
@@ -272,16 +311,18 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
 
   // ---- slots and positions
   const int n = (int)min(tokens, (int64_t)p.max_tokens);
+  int bad = 0;
 #pragma unroll 2
   for (int i = tid; i < p.max_tokens; i += kChunk) {
     if (i < n) {
       const int b = find(first, 0, p.batch, i);
-      place_token(p, i, b, first[b], sh_plan[b], (int)total);
+      bad |= place_token(p, i, b, first[b], sh_plan[b], (int)total);
     } else {
       p.slots[i] = -1;
       p.positions[i] = 0;
     }
   }
+  if (bad < 0) raise_device_error(p.err, kErrBadPage);
 }
 
 __global__ void __launch_bounds__(kSpreadThreads) k_pages_spread(const Params p) {
@@ -296,17 +337,19 @@ __global__ void __launch_bounds__(kSpreadThreads) k_pages_spread(const Params p)
     lo = find_by_warp(p.offsets, p.batch, (int)begin);
     hi = find_by_warp(p.offsets, p.batch, (int)min(begin + 32 * kSpreadTokens, (int64_t)n) - 1);
   }
+  int bad = 0;
 #pragma unroll
   for (int k = 0; k < kSpreadTokens; ++k) {
     const int64_t i = begin + 32 * k + lane;
     if (i < n) {
       const int b = find(p.offsets, lo, hi + 1, (int)i);
-      place_token(p, (int)i, b, p.offsets[b], p.plan[b], total);
+      bad |= place_token(p, (int)i, b, p.offsets[b], p.plan[b], total);
     } else if (i < p.max_tokens) {
       p.slots[i] = -1;
       p.positions[i] = 0;
     }
   }
+  if (bad < 0) raise_device_error(p.err, kErrBadPage);
 }
 
 }  // namespace plan

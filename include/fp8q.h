@@ -550,8 +550,13 @@ typedef struct {
  * 0.  The others then take pages in order.  A request is served when its table row and max_tokens
  * hold its tokens and it needs no page, or its pages and those wanted by the requests before it
  * are there; else its length stays and its tokens get slot -1.  Entries of slots past the last
- * token are -1, of positions 0.  Results do not depend on timing.  Lengths outside 0 ..
- * max_pages * page_size, counts outside 0 .. num_pages and pages given back beyond num_pages are
+ * token are -1, of positions 0.  Results do not depend on timing.  A table entry below zero stands
+ * for a page that was given away before (behind a window, say): such entries give nothing back when
+ * the request ends.  Pages recycled early must be marked so; an id left in place is given back a
+ * second time.  Where the free list, or the entry of a request's last page, holds a number below zero,
+ * the tokens of that page get slot -1 (the table -1) and device error bit 2 is raised.  Other ids are
+ * taken as they are: the append and the attention report those outside their cache.  Lengths outside
+ * 0 .. max_pages * page_size, counts outside 0 .. num_pages and pages given back beyond num_pages are
  * clipped and raise device error bit 2.  A step that failed can be repeated with the same inputs
  * (lens_out and free_count_out apart): the same pages are taken again.
  */

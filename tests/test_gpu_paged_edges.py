@@ -127,3 +127,63 @@ def test_attention_scales_of_either_sign(gran):
     pos, _ = c.run(dev_bf16(qb))
     torch.cuda.synchronize()
     assert torch.equal(neg[[0, 2]], -pos[[0, 2]])
+
+
+# ------------------------------------------------------------------ pages
+
+def update(table, lens, added, free, count, size, max_tokens):
+    """One step on copies -> (slots, served, lens, list of free pages, table, whole list)."""
+    t, f, c = dev(np.array(table, np.int32)), dev(np.array(free, np.int32)), dev(np.array([count], np.int32))
+    slots, _, _, served, lens_out, _ = fq.fp8_kv_pages_update(t, dev(np.array(lens, np.int32)), dev(np.array(added, np.int32)),
+                                                              f, c, size, max_tokens)
+    torch.cuda.synchronize()
+    n = int(host(c)[0])
+    return host(slots), host(served).tolist(), host(lens_out).tolist(), host(f)[:n].tolist(), host(t)
+
+
+@pytest.mark.parametrize("B", [4, 1300])
+def test_pages_given_away_before_are_not_given_back(B):
+    """Pages out of a window's sight were recycled early and are marked in the table: a request's end gives
+    back the others, in order, and they alone count for the list's room."""
+    table = np.full((B, 6), -1, np.int32)
+    lens, added = np.zeros(B, np.int32), np.zeros(B, np.int32)
+    table[0, :4], lens[0], added[0] = [-1, -1, 5, 6], 14, -1
+    table[1, :2], lens[1] = [7, 0], 8
+    table[B - 1, :6], lens[B - 1], added[B - 1] = [-1, 3, -2 ** 31, 4, -7, 2], 24, -1
+    slots, served, n, free, _ = update(table, lens, added, [1, 8, 0, 0, 0, 0, 0], 2, 4, 0)
+    assert free == [1, 8, 5, 6, 3, 4, 2] and n[0] == n[B - 1] == 0 and n[1] == 8
+    assert fq.device_status() == 0
+    # nothing but marked entries, and a list with no room left
+    table[0, :4], table[B - 1, :6] = -1, -1
+    *_, free, _ = update(table, lens, added, [1, 8], 2, 4, 0)
+    assert free == [1, 8] and fq.device_status() == 0
+    # more than the list holds, behind marked entries: the first ones fill it, the rest is reported
+    table[B - 1, :6] = [-1, 3, -1, 4, -1, 2]
+    *_, free, _ = update(table, lens, added, [1, 8, 0, 0], 2, 4, 0)
+    assert free == [1, 8, 3, 4] and fq.device_status() == 4
+
+
+def test_pages_given_away_among_many_given_back():
+    """More than a thousand pages given back in one step, a few of them marked."""
+    rng = np.random.default_rng(1)
+    B, width, size = 90, 60, 2
+    table = rng.permutation(B * width).astype(np.int32).reshape(B, width)
+    table[rng.random((B, width)) < 0.05] = -1
+    lens = rng.integers(0, width * size + 1, B).astype(np.int32)
+    added = np.where(rng.random(B) < 0.8, -1, 0).astype(np.int32)
+    want = [int(p) for b in range(B) if added[b] < 0 for p in table[b, :-(-lens[b] // size)] if p >= 0]
+    *_, free, _ = update(table, lens, added, np.zeros(B * width, np.int32), 0, size, 0)
+    assert free == want and len(want) > 1024                  # more than a thread block takes at once
+
+
+@pytest.mark.parametrize("max_tokens", [40, 5000])
+def test_pages_marked_entries_take_no_token(max_tokens):
+    """A free list, or a request's last page, that holds no page: the tokens have slot -1 and it is reported."""
+    size = 4
+    slots, _, _, _, table = update([[2, -1, -1, -1]], [3], [9], [9, 8, -5, 7], 4, size, max_tokens)
+    assert fq.device_status() == 4
+    assert slots[:9].tolist() == [11, 28, 29, 30, 31, -1, -1, -1, -1] and (slots[9:] == -1).all()
+    assert table[0].tolist() == [2, 7, -1, -1]
+    slots, _, _, _, _ = update([[2, -3, -1, -1]], [6], [4], [9, 8, 7], 3, size, max_tokens)
+    assert fq.device_status() == 4
+    assert slots[:4].tolist() == [-1, -1, 28, 29]
