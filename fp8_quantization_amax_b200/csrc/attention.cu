@@ -203,7 +203,7 @@ __device__ __forceinline__ float ex2_diff(float a, float b) {
 }
 
 __device__ __forceinline__ int clamped_len(const Params& p, int b) {
-  const int n = __ldg(p.lens + b);
+  const int n = p.lens[b];
   return (int)max((int64_t)0, min((int64_t)n, min((int64_t)p.max_pages * p.c.page_size, (int64_t)kMaxTokens)));
 }
 
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
   float vscale = 1.0f, kscale = 1.0f;
   if constexpr (!TOKEN_SCALES) {
     const int i = p.c.gran == 0 ? 0 : kvh;
-    kscale = __ldg(p.c.ks + i);
-    vscale = __ldg(p.c.vs + i);
+    kscale = p.c.ks[i];
+    vscale = p.c.vs[i];
   }
   const uint8_t* kbase = p.c.k + (int64_t)kvh * p.c.head_stride;
   const uint8_t* vbase = p.c.v + (int64_t)kvh * p.c.head_stride;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
       tok += tile_token(i, load.n);
       const uint32_t col = div_u32((uint32_t)tok, p.c.page_div);
       offs = tok - (int)(col * (uint32_t)p.c.page_size);
-      if (tok < load.n) pages = __ldg(p.table + (int64_t)load.b * p.max_pages + col);
+      if (tok < load.n) pages = p.table[(int64_t)load.b * p.max_pages + col];
     }
     used = 0;
   };
@@ -652,8 +652,8 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         const int k = t + 4 * j;
         uint4 x = make_uint4(0, 0, 0, 0), y = x;
         if (r < p.group && 16 * k < D) {
-          x = __ldg(reinterpret_cast<const uint4*>(src + 16 * k));
-          y = __ldg(reinterpret_cast<const uint4*>(src + 16 * k + 8));
+          x = *reinterpret_cast<const uint4*>(src + 16 * k);
+          y = *reinterpret_cast<const uint4*>(src + 16 * k + 8);
         }
         qb[h][j][0] = x.x, qb[h][j][1] = x.y, qb[h][j][2] = x.z, qb[h][j][3] = x.w;
         qb[h][j][4] = y.x, qb[h][j][5] = y.y, qb[h][j][6] = y.z, qb[h][j][7] = y.w;
@@ -1010,7 +1010,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
     }
     if (live && mine == 0) {
       float vs = 1.0f;
-      if constexpr (!TOKEN_SCALES) vs = __ldg(p.c.vs + (p.c.gran == 0 ? 0 : vh / p.row_tiles));
+      if constexpr (!TOKEN_SCALES) vs = p.c.vs[p.c.gran == 0 ? 0 : vh / p.row_tiles];
       const int kvh = vh / p.row_tiles, row = (vh - kvh * p.row_tiles) * 8 * NH + 8 * n + 2 * t;
       const int dim = g * VB + 2 * tile;     // o holds dims dim, dim + 1 of rows row, row + 1
 #pragma unroll

@@ -189,7 +189,7 @@ __device__ __forceinline__ uint2 codes_of(const Chunk& y, const Divisor& v) {
   return make_uint2(c.x ^ 0x80808080u, c.y ^ 0x80808080u);
 }
 
-// 8 bytes that are read once (q may be rotated in place, so not the read-only path)
+// 8 bytes that are read once (not by the read-only path, kv_pages.cuh; q may be rotated in place too)
 __device__ __forceinline__ uint2 load8(const void* p) {
   uint2 v;
   asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
@@ -232,7 +232,7 @@ __device__ __forceinline__ void rows(const Params& p, const Shared<LPR>& sh, int
   Divisor by;
   by.d = by.r = 1.0f;
   by.fast = true;
-  if (KIND != 0 && p.c.gran != 3 && own) by = divisor_of(__ldg(scales + (p.c.gran == 0 ? 0 : head)));
+  if (KIND != 0 && p.c.gran != 3 && own) by = divisor_of(scales[p.c.gran == 0 ? 0 : head]);
 
   struct Raw {
     uint2 r[2][2];
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append
   for (int i = threadIdx.x; i < nt * kMaxPairs; i += blockDim.x) {
     const int tk = i / kMaxPairs, f = i % kMaxPairs;
     if (f >= pairs) continue;
-    const unsigned long long a = (unsigned long long)(long long)__ldg(p.positions + t0 + tk) * __ldg(p.turns + f);
+    const unsigned long long a = (unsigned long long)(long long)p.positions[t0 + tk] * p.turns[f];
     float sn, cs;
     sincospif((float)(int)(a >> 32) * 0x1.0p-31f, &sn, &cs);
     sh.cosine[tk][f] = cs * p.gain;
@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append
     float4 wa = make_float4(0.0f, 0.0f, 0.0f, 0.0f), wb = wa;
     if (8 * at < p.c.head_dim) {
       const bool split = 8 * at < p.rot && !NEXT;
-      const Chunk w = unpack<NEXT>(__ldg(reinterpret_cast<const uint2*>(weight + (split ? 4 * at : 8 * at))),
-                                   __ldg(reinterpret_cast<const uint2*>(weight + (split ? pairs + 4 * at : 8 * at + 4))));
+      const Chunk w = unpack<NEXT>(*reinterpret_cast<const uint2*>(weight + (split ? 4 * at : 8 * at)),
+                                   *reinterpret_cast<const uint2*>(weight + (split ? pairs + 4 * at : 8 * at + 4)));
       wa = make_float4(w.a[0].x, w.a[0].y, w.a[1].x, w.a[1].y);
       wb = make_float4(w.b[0].x, w.b[0].y, w.b[1].x, w.b[1].y);
     }
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kSmWarps / kMaxWarps) k_append
     *reinterpret_cast<float4*>(&sh.weights[which][1][4 * at]) = wb;
   }
   if (threadIdx.x < nt) {
-    const int64_t slot = __ldg(p.slots + t0 + threadIdx.x);
+    const int64_t slot = p.slots[t0 + threadIdx.x];
     if (slot >= cache_slots) raise_device_error(p.err, kErrBadPage);
     const uint32_t page = div_u32((uint32_t)slot, p.c.page_div);
     const uint32_t off = (uint32_t)slot - page * (uint32_t)p.c.page_size;

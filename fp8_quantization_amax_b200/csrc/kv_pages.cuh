@@ -1,4 +1,8 @@
 // The paged FP8 KV cache as the kernels see it, and the small pieces the paged operators share.
+//
+// The paged kernels read global memory with plain loads only, no __ldg or ld.global.nc: those ask for memory
+// that nobody writes while the kernel lives, and as a programmatic dependent (sm100.cuh) it lives while
+// the kernel before it still writes lengths, tables, slots, queries or scales.
 #pragma once
 
 #include <cstdint>

@@ -187,3 +187,43 @@ def test_pages_marked_entries_take_no_token(max_tokens):
     slots, _, _, _, _ = update([[2, -3, -1, -1]], [6], [4], [9, 8, 7], 3, size, max_tokens)
     assert fq.device_status() == 4
     assert slots[:4].tolist() == [-1, -1, 28, 29]
+
+
+# ------------------------------------------------------------------ together
+
+def test_steps_back_to_back_equal_steps_apart():
+    """Decoding steps one after another without a pause (each kernel starts while its predecessor writes what it
+    reads) against the same steps with the device idle between any two calls."""
+    B, hq, hk, d, size, P, width, steps = 24, 32, 8, 128, 16, 400, 16, 150
+    turns, _ = fq.rope_turns(d, device="cuda")
+    x = dev_bf16(bf16(np.random.default_rng(3), steps, B, hq + 2 * hk, d))
+    added = torch.ones((steps, B), dtype=torch.int32, device="cuda")
+    added[40:, 3] = 0
+    added[60, 5] = -1
+    added[90, 7] = -1
+    got = []
+    for apart in (False, True):
+        kc, vc = (torch.zeros((P, size, hk, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros((hk, P * size), device="cuda") for _ in range(2))
+        table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+        lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        free = torch.arange(P, dtype=torch.int32, device="cuda")
+        count = torch.tensor([P], dtype=torch.int32, device="cuda")
+        out = torch.empty((steps, B, hq, d), dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty((steps, B, hq), device="cuda")
+        slots, pos = torch.empty(B, dtype=torch.int64, device="cuda"), torch.empty(B, dtype=torch.int32, device="cuda")
+        q = torch.empty((B, hq, d), dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            for call in (
+                    lambda: fq.fp8_kv_pages_update(table, lens, added[i], free, count, size, slots=slots, positions=pos),
+                    lambda: fq.fp8_kv_append(x[i, :, :hq], x[i, :, hq:hq + hk], x[i, :, hq + hk:], slots, kc, vc, ks, vs, 0, 3,
+                                             positions=pos, turns=turns, q_out=q),
+                    lambda: fq.fp8_attention_paged(q, kc, vc, ks, vs, table, lens, 0, 3, out=out[i], lse=lse[i])):
+                call()
+                if apart:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        got.append((kc, vc, ks, vs, table, lens, free, count, out, lse))
+    assert int(host(got[0][5]).max()) == steps and torch.isfinite(got[0][8]).all()
+    assert all(torch.equal(a, b) for a, b in zip(*got))

@@ -1,0 +1,20 @@
+"""Paged KV cache on the host: what the calls allow beyond the refusals of test_paged_host.py, the build,
+and rules of the kernels' source.  No call here reaches a kernel."""
+import os
+
+import pytest
+
+import fp8_quantization_amax_b200 as fq
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(fq.__file__)), "csrc")
+
+
+# ------------------------------------------------------------------ kernels' source
+
+@pytest.mark.parametrize("name", ["kv_plan.cu", "kv_append.cu", "attention.cu", "kv_pages.cuh"])
+def test_dependent_kernels_use_no_read_only_loads(name):
+    """A kernel launched as a programmatic dependent lives while the one before it still writes its inputs:
+    the read-only path (memory that nobody writes meanwhile) is not for them."""
+    with open(os.path.join(CSRC, name)) as f:
+        code = "\n".join(line.split("//")[0] for line in f)
+    assert "__ldg" not in code and "ld.global.nc" not in code and "__restrict__" not in code
