@@ -36,8 +36,8 @@ __device__ __forceinline__ uint4 dequant8(uint2 c, float s) {
 // Each thread handles 8-element pieces (8 code bytes in, 16 bf16 bytes out) of the flattened
 // tensor; the row of a piece comes from a multiply-shift division by the pieces per row.
 template <int FMT, int GRAN, int UNROLL>
-__global__ void __launch_bounds__(256) k_dequant(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
-                                                 uint16_t* __restrict__ y, uint32_t npieces, FastDiv ppr,
+__global__ void __launch_bounds__(256) k_dequant(const uint8_t* codes, const float* scales, uint16_t* y,
+                                                 uint32_t npieces, FastDiv ppr,
                                                  uint32_t rows, uint32_t nbc) {
   allow_dependent_launch();
   grid_dependency_wait();
@@ -53,14 +53,14 @@ __global__ void __launch_bounds__(256) k_dequant(const uint8_t* __restrict__ cod
         const uint32_t r = fdiv_u32(i, ppr);
         const uint32_t col = (i - r * ppr.d) * 8;
         if (GRAN == 0) {
-          s[k] = __ldg(scales);
+          s[k] = *scales;
         } else if (GRAN == 1) {
-          s[k] = __ldg(scales + (size_t)(col >> 7) * rows + r);
+          s[k] = scales[(size_t)(col >> 7) * rows + r];
         } else if (GRAN == 2) {
-          s[k] = __ldg(scales + (size_t)(r >> 7) * nbc + (col >> 7));
+          s[k] = scales[(size_t)(r >> 7) * nbc + (col >> 7)];
         } else {
           // MX: byte exponents [rows][cols / 32] (nbc = cols / 32), scale 2^(b - 127); 255 is NaN
-          const uint32_t b = __ldg(reinterpret_cast<const uint8_t*>(scales) + (size_t)r * nbc + (col >> 5));
+          const uint32_t b = reinterpret_cast<const uint8_t*>(scales)[(size_t)r * nbc + (col >> 5)];
           s[k] = __uint_as_float(b == 255u ? 0x7FC00000u : (b == 0u ? 0x00400000u : b << 23));
         }
       }
@@ -110,7 +110,7 @@ cudaError_t launch_dequant(const uint8_t* codes, const float* scales, int64_t ro
 // ============================================================================ codec
 
 template <int FMT>
-__global__ void __launch_bounds__(256) k_encode(const float* __restrict__ q, int64_t n, uint8_t* __restrict__ codes) {
+__global__ void __launch_bounds__(256) k_encode(const float* q, int64_t n, uint8_t* codes) {
   allow_dependent_launch();
   grid_dependency_wait();
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256) k_encode(const float* __restrict__ q, int
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(256) k_decode(const uint8_t* __restrict__ codes, int64_t n, float* __restrict__ out) {
+__global__ void __launch_bounds__(256) k_decode(const uint8_t* codes, int64_t n, float* out) {
   allow_dependent_launch();
   grid_dependency_wait();
   const int64_t stride = (int64_t)gridDim.x * blockDim.x;

@@ -28,9 +28,12 @@ struct Fmt<kE5M2> {
 
 // ---------------------------------------------------------------- global memory
 
+// Data that is read once.  Not by the read-only path (ld.global.nc, __ldg, const __restrict__ parameters): it
+// asks for memory that nobody writes while the kernel lives, and a programmatic dependent (sm100.cuh)
+// lives while the kernel before it still writes what it will read.
 __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -38,7 +41,7 @@ __device__ __forceinline__ uint4 ld_stream_v4(const void* p) {
 
 __device__ __forceinline__ uint2 ld_stream_v2(const void* p) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 

@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ CU
         const uint32_t buf = acc_use & 1u;
         if (!mbar_wait(&tfull[buf], (acc_use >> 1) & 1u, p.err)) break;
         tc_fence_after();
-        const float mult = __ldg(p.sA) * __ldg(p.sB);
+        const float mult = *p.sA * *p.sB;
         const uint32_t taddr = tmem_base + lane_addr + buf * BN + half * 128;
         uint32_t out[64];
 #pragma unroll
