@@ -4,7 +4,8 @@
 
 Each .cu under csrc/ compiles to an object under _build/ (in parallel, only when the source
 or a header is newer), then all objects link into fp8_quantization_amax_b200/libfp8q.so.
-csrc/torch_calls.cpp, the paged calls' checks against torch's headers, becomes _torch_calls.so.
+csrc/torch_calls.cpp, the paged calls' checks against torch's headers, becomes _torch_calls.so
+(a failure of that is raised after the library is linked).
 IEEE division and square root and no flush-to-zero: the quantizer's contract is bit-exact.
 """
 from __future__ import annotations
@@ -87,6 +88,10 @@ def _build_calls(force: bool, verbose: bool) -> None:
            "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd), flush=True)
+    try:
+        os.remove(CALLS)                     # made for another header: not to be loaded if this build fails
+    except FileNotFoundError:
+        pass
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
@@ -121,10 +126,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 raise
         return obj
 
+    # _torch_calls.so needs g++, Python's and torch's headers: where they are missing the C library is
+    # linked all the same, and the failure raised after that
     with ThreadPoolExecutor(max(1, min(len(sources) + 1, os.cpu_count() or 1))) as ex:
         calls = ex.submit(_build_calls, force, verbose)
         objs = list(ex.map(compile_one, sources))
-        calls.result()
     # the objects the library was last linked from: a source removed or added relinks it even
     # when every remaining object is older than the library
     stamp = os.path.join(BUILD, "linked_objects.txt")
@@ -144,6 +150,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(tmp, LIB)
         with open(stamp, "w") as f:
             f.write(listing)
+    calls.result()
     return LIB
 
 

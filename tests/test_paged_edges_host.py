@@ -5,6 +5,7 @@ import os
 import pytest
 
 import fp8_quantization_amax_b200 as fq
+from fp8_quantization_amax_b200 import build
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(fq.__file__)), "csrc")
 
@@ -21,3 +22,24 @@ def test_dependent_kernels_use_no_read_only_loads(name):
     assert "__ldg" not in code and "ld.global.nc" not in code
     if name != "gemm_sm100.cu":                      # (there: pointers of the cooperative launch, no dependent)
         assert "__restrict__" not in code
+
+
+# ------------------------------------------------------------------ build
+
+def test_c_library_is_built_where_the_python_calls_cannot_be(monkeypatch, tmp_path):
+    """No C++ compiler: libfp8q.so is linked, then the failure is raised; an older _torch_calls.so is gone."""
+    build.build()
+    lib, calls = tmp_path / "lib.so", tmp_path / "calls.so"
+    calls.write_bytes(b"of another header")
+    os.utime(calls, (1, 1))
+    monkeypatch.setattr(build, "LIB", str(lib))
+    monkeypatch.setattr(build, "CALLS", str(calls))
+    monkeypatch.setenv("CXX", "/bin/false")
+    with pytest.raises(RuntimeError, match="torch_calls"):
+        build.build()
+    assert lib.stat().st_size > 1 << 20 and not calls.exists()
+    monkeypatch.setenv("CXX", str(tmp_path / "missing"))
+    lib.unlink()
+    with pytest.raises(FileNotFoundError):
+        build.build()
+    assert lib.stat().st_size > 1 << 20
