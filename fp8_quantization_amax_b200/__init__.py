@@ -800,10 +800,12 @@ def fp8_kv_pages_update(block_table: torch.Tensor, lens: torch.Tensor, added: to
 
 
 def rope_turns(rot_dim: int, base: float = 10000.0, kind: int = ROPE_PLAIN, factor: float = 1.0,
-               original_len: float = 8192.0, low: float = 1.0, high: float = 4.0, device=None):
+               original_len: float = 8192.0, low: float = 1.0, high: float | None = None, device=None):
     """Rotary frequencies for fp8_kv_append: (turns int64 [rot_dim / 2] holding 64-bit fractions of a
     turn per position, gain).  Host only; the tensor is made on `device`.  See fp8q_rope_turns in
-    include/fp8q.h for the kinds."""
+    include/fp8q.h for the kinds.  high when not given: 32 for ROPE_RAMP, else 4."""
+    if high is None:
+        high = 32.0 if kind == ROPE_RAMP else 4.0
     host = torch.empty(rot_dim // 2 if rot_dim > 0 else 0, dtype=torch.int64)
     gain = ctypes.c_float()
     _check("fp8q_rope_turns", lib().fp8q_rope_turns(rot_dim, base, kind, factor, original_len, low, high,

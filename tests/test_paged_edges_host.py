@@ -3,6 +3,7 @@ and rules of the kernels' source.  No call here reaches a kernel."""
 import os
 
 import pytest
+import torch
 
 import fp8_quantization_amax_b200 as fq
 from fp8_quantization_amax_b200 import build
@@ -22,6 +23,18 @@ def test_dependent_kernels_use_no_read_only_loads(name):
     assert "__ldg" not in code and "ld.global.nc" not in code
     if name != "gemm_sm100.cu":                      # (there: pointers of the cooperative launch, no dependent)
         assert "__restrict__" not in code
+
+
+# ------------------------------------------------------------------ rotation table
+
+def test_rope_turns_defaults_follow_the_kind():
+    """`high` left out: 4 turns for the smooth kind, 32 for the ramp (the value of the paper it follows)."""
+    for kind, high in ((fq.ROPE_SMOOTH, 4.0), (fq.ROPE_RAMP, 32.0)):
+        got, gain = fq.rope_turns(128, 500000.0, kind, 8.0)
+        want, same = fq.rope_turns(128, 500000.0, kind, 8.0, 8192.0, 1.0, high)
+        assert torch.equal(got, want) and gain == same
+        other, _ = fq.rope_turns(128, 500000.0, kind, 8.0, 8192.0, 1.0, 36.0 - high)
+        assert not torch.equal(got, other)
 
 
 # ------------------------------------------------------------------ build
