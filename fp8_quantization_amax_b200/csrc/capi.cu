@@ -2,9 +2,8 @@
 // Every check happens on the host before anything is launched.
 #include <cuda_runtime.h>
 
-#include <cstdint>
-
 #include <cmath>
+#include <cstdint>
 
 #include "fp8q.h"
 #include "internal.h"
@@ -43,19 +42,22 @@ constexpr int64_t kMaxSpan = int64_t(1) << 36;                 // bytes of a pag
 fp8q_status paged_cache(const fp8q_kv_pages* c, fp8q::KvPages* out) {
   if (!c || !valid_fmt(c->f) || c->g < FP8Q_KV_PER_TENSOR || c->g > FP8Q_KV_PER_TOKEN) return FP8Q_ERR_INVALID_ARGUMENT;
   if (c->num_pages < 0 || c->page_size < 1 || c->heads < 1 || c->head_dim < 1) return FP8Q_ERR_INVALID_ARGUMENT;
-  if (c->head_dim % 16 != 0 || c->page_stride % 16 != 0 || c->token_stride % 16 != 0 || c->head_stride % 16 != 0)
+  // strides of dimensions of one entry are not used
+  const int64_t page_stride = c->num_pages > 1 ? c->page_stride : 0, token_stride = c->page_size > 1 ? c->token_stride : 0,
+                head_stride = c->heads > 1 ? c->head_stride : 0;
+  if (c->head_dim % 16 != 0 || page_stride % 16 != 0 || token_stride % 16 != 0 || head_stride % 16 != 0)
     return FP8Q_ERR_INVALID_ARGUMENT;
   if (c->head_dim > 256 || c->heads > 65536 || c->page_size > kMaxTableTokens ||
       (c->num_pages > 0 && c->page_size > kMaxTableTokens / c->num_pages))
     return FP8Q_ERR_UNSUPPORTED;
   // the last code's place, in units of 16 bytes, fits 32 bits (64 GB a tensor)
-  if (c->page_stride > kMaxSpan || c->token_stride > kMaxSpan || c->head_stride > kMaxSpan ||
-      c->page_stride * (double)c->num_pages + c->token_stride * (double)c->page_size + c->head_stride * (double)c->heads >
+  if (page_stride > kMaxSpan || token_stride > kMaxSpan || head_stride > kMaxSpan ||
+      page_stride * (double)c->num_pages + token_stride * (double)c->page_size + head_stride * (double)c->heads >
           (double)kMaxSpan)
     return FP8Q_ERR_UNSUPPORTED;
   // places of different tokens, heads or pages do not overlap
-  if ((c->heads > 1 && c->head_stride < c->head_dim) || (c->page_size > 1 && c->token_stride < c->head_dim) ||
-      (c->num_pages > 1 && c->page_stride < c->head_dim))
+  if ((c->heads > 1 && head_stride < c->head_dim) || (c->page_size > 1 && token_stride < c->head_dim) ||
+      (c->num_pages > 1 && page_stride < c->head_dim))
     return FP8Q_ERR_INVALID_ARGUMENT;
   if (!c->k_scales || !c->v_scales || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
     return FP8Q_ERR_INVALID_ARGUMENT;
@@ -65,9 +67,9 @@ fp8q_status paged_cache(const fp8q_kv_pages* c, fp8q::KvPages* out) {
   out->v = c->v_codes;
   out->ks = c->k_scales;
   out->vs = c->v_scales;
-  out->page_stride = c->page_stride;
-  out->token_stride = c->token_stride;
-  out->head_stride = c->head_stride;
+  out->page_stride = page_stride;
+  out->token_stride = token_stride;
+  out->head_stride = head_stride;
   out->num_pages = (int)c->num_pages;
   out->page_size = (int)c->page_size;
   out->heads = (int)c->heads;

@@ -7,8 +7,30 @@ import torch
 
 import fp8_quantization_amax_b200 as fq
 from fp8_quantization_amax_b200 import build
+from test_paged_host import append_args, attention_args, pages
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(fq.__file__)), "csrc")
+
+
+# ------------------------------------------------------------------ refusals
+
+def cache_status(**kw):
+    """Status of an append and an attention that have nothing to do, so that the cache alone decides."""
+    L, cache = fq.lib(), pages(**kw)
+    got = {L.fp8_kv_append(*append_args(cache, tokens=0)), L.fp8_attention_paged(*attention_args(cache, batch=0))}
+    assert len(got) == 1
+    return got.pop()
+
+
+@pytest.mark.parametrize("single,change,status", [
+    ("head", {}, 0), ("token", {}, 0), ("page", {}, 0), ("head", dict(page_stride=1 << 35), 2),
+    ("token", dict(page_stride=1 << 35), 2), ("page", dict(token_stride=1 << 33), 2),
+])
+@pytest.mark.parametrize("unused", [-(1 << 46), -16, 0, 8, 1 << 50])
+def test_strides_of_single_entries_are_not_used(single, change, status, unused):
+    """Neither refused nor, negative, counted against the others' span."""
+    d = {"head": dict(heads=1), "token": dict(page_size=1), "page": dict(num_pages=1)}[single]
+    assert cache_status(**{**d, single + "_stride": unused, **change}) == status
 
 
 # ------------------------------------------------------------------ kernels' source
