@@ -2,6 +2,7 @@
 // Every check happens on the host before anything is launched.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -55,10 +56,18 @@ fp8q_status paged_cache(const fp8q_kv_pages* c, fp8q::KvPages* out) {
       page_stride * (double)c->num_pages + token_stride * (double)c->page_size + head_stride * (double)c->heads >
           (double)kMaxSpan)
     return FP8Q_ERR_UNSUPPORTED;
-  // places of different tokens, heads or pages do not overlap
-  if ((c->heads > 1 && head_stride < c->head_dim) || (c->page_size > 1 && token_stride < c->head_dim) ||
-      (c->num_pages > 1 && page_stride < c->head_dim))
-    return FP8Q_ERR_INVALID_ARGUMENT;
+  // places of different tokens, heads and pages do not overlap: taken by their strides, each dimension steps
+  // over all that lies within one entry of it
+  struct Dim {
+    int64_t stride, n;
+  } dims[3] = {{page_stride, c->num_pages}, {token_stride, c->page_size}, {head_stride, c->heads}};
+  std::sort(dims, dims + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t within = c->head_dim;              // bytes from the first to the last code of an entry
+  for (const Dim& d : dims) {
+    if (d.n <= 1) continue;
+    if (d.stride < within) return FP8Q_ERR_INVALID_ARGUMENT;
+    within += (d.n - 1) * d.stride;          // (at most kMaxSpan)
+  }
   if (!c->k_scales || !c->v_scales || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
     return FP8Q_ERR_INVALID_ARGUMENT;
   if (c->num_pages > 0 && (!c->k_codes || !c->v_codes || !aligned(c->k_codes, 16) || !aligned(c->v_codes, 16)))

@@ -518,7 +518,8 @@ FP8Q_API fp8q_status fp8_gemm_mx(const uint8_t *A, const uint8_t *sA, fp8q_forma
  *            FP8Q_KV_PER_HEAD_TOK128  scales [ceil(S/128)][heads], of 128 consecutive slots
  *            FP8Q_KV_PER_TOKEN        scales [heads][S] (the 1x128 layout of [W] 激活动态量化 where
  *                                     head_dim is 128: a head's token scales are contiguous)
- * Requirements: head_dim a multiple of 16, at most 256; strides multiples of 16 bytes; code
+ * Requirements: head_dim a multiple of 16, at most 256; strides (of dimensions of more than one entry)
+ * multiples of 16 bytes, each stepping over all that lies within one entry of its dimension; code
  * pointers 16-byte aligned; num_pages * page_size below 2^31 - 64, K and V at most 64 GB each.
  */
 typedef struct {

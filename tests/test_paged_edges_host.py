@@ -33,6 +33,18 @@ def test_strides_of_single_entries_are_not_used(single, change, status, unused):
     assert cache_status(**{**d, single + "_stride": unused, **change}) == status
 
 
+@pytest.mark.parametrize("page,token,head,status", [
+    (2048, 128, 64, 0), (2048, 64, 1024, 0), (64, 512, 256, 0), (64, 256, 4096, 0), (4096, 256, 128, 0), (8192, 80, 4096, 0),
+    (2048, 64, 64, 1), (2048, 128, 128, 1), (2048, 64, 960, 1), (1024, 128, 64, 1), (128, 128, 64, 1), (64, 240, 64, 1),
+    (64, 256, 4000, 1), (2032, 128, 64, 1),
+])
+def test_layouts_whose_places_overlap_are_refused(page, token, head, status):
+    """4 pages of 16 tokens of 2 heads of 64, whichever order the dimensions lie in."""
+    assert cache_status(page_stride=page, token_stride=token, head_stride=head) == status
+    places = sorted(p * page + t * token + h * head for p in range(4) for t in range(16) for h in range(2))
+    assert status == int(any(b - a < 64 for a, b in zip(places, places[1:])))
+
+
 # ------------------------------------------------------------------ kernels' source
 
 @pytest.mark.parametrize("name", ["kv_plan.cu", "kv_append.cu", "attention.cu", "kv_pages.cuh", "dequantize.cu", "quantize.cu",
