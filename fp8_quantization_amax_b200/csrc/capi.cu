@@ -638,7 +638,9 @@ size_t fp8q_attention_workspace_bytes(int64_t batch, int64_t max_tokens, int64_t
 }
 
 int fp8q_check_attention_split(const int32_t* lens, int64_t batch, int64_t window, int64_t sinks, int workers) {
-  if (window > kMaxTableTokens || sinks > kMaxTableTokens) return -1;
+  if (window > kMaxTableTokens || sinks > kMaxTableTokens || (batch > 0 && !lens)) return -1;
+  for (int64_t b = 0; b < batch; ++b)
+    if (lens[b] < 0 || lens[b] > kMaxTableTokens) return -1;
   return fp8q::check_attention_split(lens, batch, (int)window, (int)sinks, workers);
 }
 

@@ -59,6 +59,15 @@ def test_dependent_kernels_use_no_read_only_loads(name):
         assert "__restrict__" not in code
 
 
+# ------------------------------------------------------------------ division of the attention's work
+
+@pytest.mark.parametrize("n", [-1, -2 ** 31, 2 ** 31 - 1, 2 ** 31 - 64])
+def test_attention_split_refuses_lengths_that_no_call_has(n):
+    """Tokens are counted in an int up to 2^31 - 65: beyond, the count of tiles itself would overflow."""
+    assert fq.check_attention_split([5, n], 0, 0, 148) == -1
+    assert fq.check_attention_split([n, 5], 100, 4, 148) == -1
+
+
 # ------------------------------------------------------------------ rotation table
 
 def test_rope_turns_defaults_follow_the_kind():
