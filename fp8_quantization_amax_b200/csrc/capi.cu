@@ -574,6 +574,7 @@ fp8q_status fp8q_rope_turns(int64_t rot_dim, double base, fp8q_rope_kind kind, d
       const double stretch = std::fmin(1.0, std::fmax(0.0, ((double)i - from) / (to - from)));
       f = (1.0 - stretch) * f + stretch * f / factor;
     }
+    if (!std::isfinite(f)) return FP8Q_ERR_INVALID_ARGUMENT;         // (base below 1e-300 or so)
     const double turn = f / two_pi;
     // the fraction of a turn in units of 2^-64 (positions are whole numbers: whole turns vanish)
     turns[i] = (uint64_t)std::nearbyint(std::ldexp(turn - std::floor(turn), 64));

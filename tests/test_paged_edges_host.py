@@ -80,6 +80,15 @@ def test_rope_turns_defaults_follow_the_kind():
         assert not torch.equal(got, other)
 
 
+@pytest.mark.parametrize("kind", [fq.ROPE_PLAIN, fq.ROPE_LINEAR, fq.ROPE_SMOOTH])
+def test_rope_turns_refuses_frequencies_beyond_doubles(kind):
+    with pytest.raises(fq.Fp8qError) as e:
+        fq.rope_turns(256, 5e-324, kind, 2.0)
+    assert e.value.status == 1
+    turns, _ = fq.rope_turns(256, 1e-300, kind, 2.0)         # the largest frequency is 10^297 and finite
+    assert turns.numel() == 128
+
+
 # ------------------------------------------------------------------ build
 
 def test_c_library_is_built_where_the_python_calls_cannot_be(monkeypatch, tmp_path):
