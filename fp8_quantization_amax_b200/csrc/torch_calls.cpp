@@ -125,8 +125,9 @@ struct Cache {
     c.page_stride = c.num_pages > 1 ? k.stride(0) : 0;
     c.token_stride = c.page_size > 1 ? k.stride(1) : 0;
     c.head_stride = c.heads > 1 ? k.stride(2) : 0;
-    const int64_t gran = integer(o[5]), slots = c.num_pages * c.page_size;
-    c.f = (fp8q_format)integer(o[4]);
+    const int64_t fmt = integer(o[4]), gran = integer(o[5]), slots = c.num_pages * c.page_size;
+    if (fmt != FP8Q_E4M3 && fmt != FP8Q_E5M2) wrong_value("fmt must be one of E4M3, E5M2");
+    c.f = (fp8q_format)fmt;
     c.g = (fp8q_kv_granularity)gran;
     const int64_t one[1] = {1}, head[1] = {c.heads}, blocks[2] = {(slots + 127) / 128, c.heads}, each[2] = {c.heads, slots};
     if (gran < 0 || gran > 3) wrong_value("gran must be one of KV_PER_TENSOR, KV_PER_HEAD, KV_PER_HEAD_TOK128, KV_PER_TOKEN");

@@ -45,6 +45,17 @@ def test_layouts_whose_places_overlap_are_refused(page, token, head, status):
     assert status == int(any(b - a < 64 for a, b in zip(places, places[1:])))
 
 
+@pytest.mark.parametrize("fmt", [2, -1, 1 << 32, (1 << 32) + 1, -(1 << 40)])
+def test_formats_that_are_none_are_refused(fmt):
+    """Not cut to 32 bits first, which made 2^32 the format 0."""
+    k, s = torch.empty((4, 16, 2, 64), dtype=torch.uint8), torch.empty(2)
+    x, n = torch.empty((3, 2, 64), dtype=torch.bfloat16), torch.empty(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="fmt"):
+        fq.fp8_attention_paged(x, k, k, s, s, torch.empty((3, 5), dtype=torch.int32), n, fmt)
+    with pytest.raises(ValueError, match="fmt"):
+        fq.fp8_kv_append(None, x, x, n.long(), k, k, s, s, fmt)
+
+
 # ------------------------------------------------------------------ kernels' source
 
 @pytest.mark.parametrize("name", ["kv_plan.cu", "kv_append.cu", "attention.cu", "kv_pages.cuh", "dequantize.cu", "quantize.cu",
