@@ -12,7 +12,7 @@
 // Every code is exact in f16, and so is a query (bf16) times a power of two of its row, but for elements
 // below 2^-31 of the row's largest (off by at most 2^-39 of that).  The softmax weights are rounded to f16:
 // half a step is 2^-11 of a weight, below the output's bf16 2^-8, and 2^-34 of the row's largest weight where
-// that is more (kLift).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
+// that is more (kUp).  Query rows fill 8 of a tile's rows, so a 128-row tcgen05 tile would be 6 % full.
 //
 //   S^T (token x query): A = K (rows: 16 tokens), B = q (columns: 8 query heads)
 //   O^T (dim x query):   A = V^T (rows: 16 dims),  B = P^T (columns: 8 query heads)
@@ -75,13 +75,14 @@ constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers s
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
 constexpr int kJoinBatch = 8;                 // parts whose loads are in flight together
-// The reference lies kLift (base 2) below the maximum that set it and follows when a score exceeds that
-// maximum by kSlack, so a row's largest weight is 2^kLift .. 2^(kLift + kSlack) (f16 ends at 2^16) and what f16
-// rounds away of small ones is at most 2^-(25 + kLift) of the largest.  With the reference at the maximum, 8192
-// tokens of weight 2^-26 beside one of V = 0 gave 0.  us at slacks 8 / 6 / 4 / 2: window 17.6 17.6 17.9 18.5,
-// one kv head 27.1 26.8 27.4 27.5, the other cases alike.
-constexpr float kLift = 9.0f, kSlack = 6.0f;
-static_assert(kLift + kSlack < 16.0f, "weights fit f16");
+// A weight is 1 at the running maximum m, which follows the scores when one exceeds it by 2^kSlack.  For f16
+// (2^16 at most) weights are taken times kUp = 2^9, so a row's largest is 2^9 .. 2^(9 + kSlack) and what the
+// rounding takes from small ones is at most 2^-34 of it (without the factor, 8192 tokens of weight
+// 2^-26 beside one of V = 0 gave 0).  The sum l is of the weights themselves and m the maximum itself, so that
+// lse does not lose the bits that a shifted score would have to give up.
+// us at slacks 8 / 6 / 4 / 2: window 17.6 17.6 17.9 18.5, one kv head 27.1 26.8 27.4 27.5, the other cases alike.
+constexpr float kUp = 512.0f, kDown = 1.0f / kUp, kSlack = 6.0f;
+static_assert(kUp * 64.0f < 65504.0f, "weights fit f16");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -159,7 +160,7 @@ __device__ __forceinline__ float lds32(uint32_t addr) {
 }
 
 // 2^x.  Results below 2^-126 become zero unless FULL: that takes four instructions in place of one.
-// Without scales of single tokens the largest weight of a row is at least 2^kLift and what
+// Without scales of single tokens the largest weight of a row is at least 1 and what
 // vanishes does not show; a token's scale joins the reference, so with them all weights may be small.
 template <bool FULL>
 __device__ __forceinline__ float ex2(float x) {
@@ -294,7 +295,7 @@ __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, in
     for (int e = 0; e < 2; ++e) {
       const int r = r0 + 8 * n + 2 * t + e;
       if (r >= p.group) continue;
-      const float l = s.l[n][e], f = vs * rcp(l);
+      const float l = s.l[n][e], f = vs * (kDown * rcp(l));
       if (p.lse && g == 0)
         p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] =
             l == 0.0f ? -INFINITY : kLn2 * (s.m[n][e] + lg2(l));
@@ -775,13 +776,13 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
           }
       }
       // The magnitude of V's scale counts towards the reference, so that a weight times its scale fits f16
-      // (one below 2^-60 counts as that: the weight itself, at most 2^75 then, has to fit fp32)
+      // (one below 2^-60 counts as that: the weight itself, at most 2^66 then, has to fit fp32)
       bool above = false;
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          above |= (TOKEN_SCALES ? st[h][e] + vl[e >> 1] : st[h][e]) > s.m[h][e & 1] + (kLift + kSlack);
+          above |= (TOKEN_SCALES ? st[h][e] + vl[e >> 1] : st[h][e]) > s.m[h][e & 1] + kSlack;
       if (__any_sync(0xFFFFFFFFu, above)) {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
@@ -791,7 +792,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
             top[e] = TOKEN_SCALES ? fmaxf(st[h][e] + vl[0], st[h][2 + e] + vl[1]) : fmaxf(st[h][e], st[h][2 + e]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], d));
-            top[e] = fmaxf(top[e] - kLift, s.m[h][e]);
+            top[e] = fmaxf(top[e], s.m[h][e]);
           }
           s.rescale(h, ex2_diff<TOKEN_SCALES>(s.m[h][0], top[0]), ex2_diff<TOKEN_SCALES>(s.m[h][1], top[1]));
           s.m[h][0] = top[0];
@@ -804,11 +805,13 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
         const float m0 = s.m[h][0] == -INFINITY ? 0.0f : s.m[h][0], m1 = s.m[h][1] == -INFINITY ? 0.0f : s.m[h][1];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float a = ex2<TOKEN_SCALES>(st[h][2 * k] - m0), e = ex2<TOKEN_SCALES>(st[h][2 * k + 1] - m1);
+          const float a = ex2<TOKEN_SCALES>(st[h][2 * k] - m0), e = ex2<TOKEN_SCALES>(st[h][2 * k + 1] - m1);
           s.l[h][0] += a;
           s.l[h][1] += e;
-          if constexpr (TOKEN_SCALES) a *= vf[k], e *= vf[k];
-          pb[h][k] = transpose8(pack_f16(a, e));
+          float2 w = make_float2(a, e);
+          if constexpr (TOKEN_SCALES) w = __fmul2_rn(w, make_float2(vf[k], vf[k]));
+          w = __fmul2_rn(w, make_float2(kUp, kUp));
+          pb[h][k] = transpose8(pack_f16(w.x, w.y));
         }
       }
 
@@ -1016,7 +1019,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         if (row + r >= p.group) continue;
-        const float l = r ? l1 : l0, m = r ? m1 : m0, f = vs * rcp(l);
+        const float l = r ? l1 : l0, m = r ? m1 : m0, f = vs * (kDown * rcp(l));
         const int64_t head = kvh * p.group + row + r;
         if (p.lse && tile == 0 && g == 0)
           p.lse[(int64_t)e.x * (p.c.heads * p.group) + head] = l == 0.0f ? -INFINITY : kLn2 * (m + lg2(l));

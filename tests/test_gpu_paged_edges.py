@@ -10,9 +10,9 @@ import torch
 import fp8_quantization_amax_b200 as fq
 import paged_reference as ref
 from helpers import dev, dev_bf16, host
-from test_gpu_paged import Cache, append_case, bf16
+from test_gpu_paged import Cache, append_case, attend, bf16
 
-#: the largest weight of a row is at least 2^LIFT when weights are rounded to f16
+#: weights are rounded to f16 after a factor that makes a row's largest 2^LIFT at least
 LIFT = 9
 
 pytestmark = pytest.mark.gpu
@@ -127,6 +127,17 @@ def test_attention_scales_of_either_sign(gran):
     pos, _ = c.run(dev_bf16(qb))
     torch.cuda.synchronize()
     assert torch.equal(neg[[0, 2]], -pos[[0, 2]])
+
+
+@pytest.mark.parametrize("seed,lens,heads,group,d,size,fmt,gran,window,sinks,layout", [
+    (251924, [9, 1, 9, 9, 1], 11, 9, 16, 5, 1, 3, 0, 0, "htd"),
+    (238364, [1, 0, 5, 9, 9, 1], 33, 17, 16, 16, 0, 3, 0, 0, "thd"),
+    (7, [1] * 40, 16, 1, 48, 32, 1, 2, 0, 0, "htd"),
+    (8, list(range(60)), 16, 3, 48, 16, 1, 3, 8, 17, "thd"),
+])
+def test_attention_lse_of_few_tokens(seed, lens, heads, group, d, size, fmt, gran, window, sinks, layout):
+    """The sum of few weights near 1 is what their logarithm is taken of: factors for f16 do not enter it."""
+    attend(seed, lens, heads, group, d, size, fmt, gran, window, sinks, layout)
 
 
 # ------------------------------------------------------------------ pages
