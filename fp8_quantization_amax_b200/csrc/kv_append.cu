@@ -137,11 +137,12 @@ __device__ __forceinline__ Divisor divisor_of(float s) {
 }
 
 // RN(x / d) with r = RN(1 / d) (Markstein's step, fp8q_device.cuh: correct for every bf16 x, and to
-// the last place for other x), d of ordinary size; an overflowing quotient stays infinite and saturates
+// the last place for other x), d of ordinary size; an overflowing quotient stays infinite and saturates,
+// a zero keeps its sign
 __device__ __forceinline__ float quotient(float x, float d, float r) {
   const float q0 = __fmul_rn(x, r);
   const float q = __fmaf_rn(-__fmaf_rn(q0, d, -x), r, q0);
-  return fabsf(q0) < 0x1.0p100f ? q : q0;
+  return q0 != 0.0f && fabsf(q0) < 0x1.0p100f ? q : q0;
 }
 
 // Codes for any divisor, without a division: a tiny or huge one is moved to ordinary size by a power

@@ -9,7 +9,7 @@ import torch
 
 import fp8_quantization_amax_b200 as fq
 import paged_reference as ref
-from helpers import dev, dev_bf16, host
+from helpers import assert_codes_equal, dev, dev_bf16, host
 from test_gpu_paged import Cache, append_case, attend, bf16
 
 #: weights are rounded to f16 after a factor that makes a row's largest 2^LIFT at least
@@ -53,6 +53,27 @@ def test_append_after_nan_in_shared_memory(d, interleaved, monkeypatch):
     monkeypatch.setattr(fq, "fp8_kv_append", after_nan)
     for rot in (0, d // 2 // 8 * 8, d):
         append_case(d + rot, 700, 3, 3, d, 24, 0, 3, rot, interleaved, True)
+
+
+def test_append_given_scales_of_every_kind(orc):
+    """All bf16 inputs by scales at the borders of the kernel's division (2^-68, 2^-60, 2^100, 2^119), tiny, huge,
+    negative, infinite and NaN: FP8 of the fp32 quotient, and signed zeros for a scale of zero."""
+    s = np.array([1.0, 0.3, -0.5, -3e-3, 0.0, -0.0, np.inf, -np.inf, np.nan, 1e-40, -1e-40, 1e-45, 3e38, -3e38, 2.0 ** -126,
+                  2.0 ** -69, 2.0 ** -68, 2.0 ** -60, 2.0 ** 100, 2.0 ** 101, 2.0 ** 119, 2.0 ** 120], np.float32)
+    H, D, T = len(s), 256, 256
+    x = np.broadcast_to(np.arange(T * D).astype(np.uint16).reshape(T, 1, D), (T, H, D))
+    xf = (x.astype(np.uint32) << 16).view(np.float32)
+    with np.errstate(all="ignore"):
+        q = np.where(s[None, :, None] == 0, np.copysign(np.float32(0), xf), xf / s[None, :, None]).astype(np.float32)
+    for fmt in (0, 1):
+        k = torch.zeros((T // 16, 16, H, D), dtype=torch.uint8, device="cuda")
+        v = torch.zeros_like(k)
+        fq.fp8_kv_append(None, dev_bf16(x), dev_bf16(x), torch.arange(T, device="cuda"), k, v, dev(s), dev(s), fmt, 1)
+        torch.cuda.synchronize()
+        want = orc.encode(np.ascontiguousarray(q).reshape(-1), fmt).reshape(T, H, D)
+        for h in range(H):
+            assert_codes_equal(host(v).reshape(T, H, D)[:, h], want[:, h], fmt, f"scale {s[h]}")
+        assert torch.equal(k, v)
 
 
 # ------------------------------------------------------------------ attention
