@@ -66,8 +66,8 @@ constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one
 // least share of a block, in tiles (1: 11.4 us for one request of 1500 tokens against 10.6; 4: 11.1)
 constexpr int kMinTiles = 2;
 constexpr int kWholeTiles = 4;                // requests of fewer tiles a warp are not divided
-constexpr int kSpreadTiles = 48;              // few requests of so many tiles have their heads spread ...
-constexpr int kSpreadPhases = 12;             // ... with so many warps a head at most
+constexpr int kSpreadRounds = 4;              // few requests of so many tiles a warp have their heads spread,
+constexpr int kSpreadPhases = 12;             // with so many warps a head at most (shape_of)
 constexpr int64_t kMaxCost = 0x7FFFFFFF;      // of all requests
 // a change of request, in tiles of a phase (16 ragged requests: 0 24.9 us, 1 23.2, 2 22.2, 3 21.6, 4 21.8)
 constexpr int kTurn = 3;
@@ -329,9 +329,9 @@ __device__ __forceinline__ int swizzled(int row, int c) {
 template <int DP>
 constexpr int kStageBytes = 2 * kAttnTile * DP + 2 * kAttnTile * 4;
 
-// One block per SM.  Up to 128 registers a thread 16 warps share an SM (8 warps at the same shapes: 117
-// against 106 us for 64 requests of up to 8192 tokens, 24.4 against 25.0 for 16 of up to 4096); two row
-// tiles of 128 dims or one of 256 need more, and 8 warps.
+// One block per SM.  Up to 128 registers a thread 16 warps share an SM (us with 16 / with 8 warps: 64 requests of
+// up to 8192 tokens 112.0 / 123.4, one of 131072 57.5 / 64.4, 16 of up to 4096 21.7 / 21.9); two row tiles of 128
+// dims or one of 256 need more, and 8 warps.
 __host__ __device__ constexpr int warps_of(int dp, int nh) { return dp * nh <= 128 ? 16 : 8; }
 // Two row tiles of 256 dims leave no registers for the query fragments: they lie in shared memory, each
 // thread's own, beside two stages.  Else as many stages as fit in about 200 KB, at most 6
@@ -1069,12 +1069,16 @@ inline Shape shape_of(int64_t batch, int64_t max_tokens, int heads, int group, i
   // begin, and there is no second launch.  us whole / divided (8 heads of 128, two warps each): 300 requests
   // of up to 100 tokens 21.2 / 24.2, but one of 160 (5 tiles a warp) 10.4 / 9.5.
   s.whole = tiles <= kWholeTiles * s.phases;
-  // Where each request can have blocks of its own for one head or a few, its heads are spread over the
-  // machine and it stays whole up to kSpreadTiles.  us spread / else, 8 heads of 128: one request of 33
-  // tokens 4.5 / 7.0, of 500 8.3 / 10.1, of 750 9.7 / 10.5, of 1000 11.6 / 10.7; 16 of up to 500 8.4 / 11.8, of up
-  // to 750 9.8 / 12.8; one head of 256, 500 tokens 11.0 / 11.0.  With 8 warps a head at most 16 of up to 500
-  // take 9.5, with 6 10.1.
-  if (tiles <= kSpreadTiles)
+  // Where each request can have blocks of its own for one head or a few, its heads are spread over the machine
+  // and it stays whole up to kSpreadRounds tiles of each of a head's warps: 48 tiles where a block has 16 warps,
+  // 32 where it has 8.  us spread / else, by heads x query heads of a head x dims.  16 warps: 8 x 4 x 128, one request
+  // of 33 tokens 4.4 / 7.0, 500 8.3 / 10.1, 750 9.7 / 10.5, 1000 11.6 / 10.7, 16 of up to 750 9.8 / 12.8; one of 750,
+  // 1 x 8 x 128 9.6 / 10.3, 2 x 8 x 64 7.4 / 8.7, 32 x 1 x 128 9.6 / 12.3.  8 warps: 1 x 16 x 256, one of 500 14.4 / 14.4,
+  // 750 16.9 / 12.4; 8 x 12 x 128, 500 10.4 / 11.2, 750 12.0 / 10.8 (but 16 of up to 750 12.1 / 14.1); 4 x 4 x 256, 250
+  // 8.3 / 9.3, 500 10.9 / 9.5, 16 of up to 500 10.9 / 11.1, one of 750 13.1 / 9.9.  With at most 6 or 16 warps a head
+  // nearly all take as long or longer (8 x 1 x 64, 16 of up to 500: 7.8 and 7.3 against 6.7).
+  const int most_warps = std::min(warps, kSpreadPhases);
+  if (tiles <= kSpreadRounds * most_warps)
     for (int heads = 1; heads <= s.heads_per_block; ++heads) {
       const int groups = (s.vheads + heads - 1) / heads;
       if (batch * groups > sms) continue;

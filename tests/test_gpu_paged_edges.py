@@ -161,6 +161,14 @@ def test_attention_lse_of_few_tokens(seed, lens, heads, group, d, size, fmt, gra
     attend(seed, lens, heads, group, d, size, fmt, gran, window, sinks, layout)
 
 
+@pytest.mark.parametrize("most", [511, 512, 513, 768, 769])
+@pytest.mark.parametrize("heads,group,d", [(4, 4, 256), (8, 12, 128), (1, 16, 256), (2, 3, 160)])
+def test_attention_wide_heads_spread(heads, group, d, most):
+    """Blocks of 8 warps around the lengths up to which heads are spread and requests stay whole."""
+    attend(most, [most, 3, most // 2], heads, group, d, 16, 0, 1, max_pages=-(-most // 16))
+    attend(most + 1, [most], heads, group, d, 24, 1, 3, max_pages=-(-most // 24))
+
+
 # ------------------------------------------------------------------ pages
 
 def update(table, lens, added, free, count, size, max_tokens):
