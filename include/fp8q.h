@@ -108,8 +108,10 @@ FP8Q_API int fp8q_version(void);
  * 0: no error.  Bit 0: a bounded wait inside a kernel (a pipeline barrier that never completed)
  * gave up after its time limit, so that kernel's outputs are incomplete.  Bit 1: a GEMM
  * workspace was not zero-filled (see fp8_gemm_blockscaled), so some output tiles were not
- * written.  Bit 2: a paged KV-cache call met a page, slot, length or free-page count outside the
- * cache; memory outside it was neither read nor written.  0xFFFFFFFF: the device could not be queried (e.g. an earlier fault).
+ * written.  Bit 2: a paged KV-cache call met a page, slot or free-page count outside the cache, or
+ * fp8_kv_pages_update a length outside its table; memory outside the cache was neither read nor
+ * written.  (fp8_attention_paged clips lengths without reporting them.)  0xFFFFFFFF: the device could
+ * not be queried (e.g. an earlier fault).
  */
 FP8Q_API uint32_t fp8q_device_status(void);
 
@@ -636,7 +638,8 @@ FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_pages *cache, const void *q, in
  *                 same time need separate ones
  * A request of length 0 gives zeros and lse = -inf.  Codes and scales of tokens that are not
  * visible, whatever they hold, do not reach the result.  A visible token's page outside the cache is
- * read as zeros and raises device error bit 2; lengths are clipped to 0 .. max_pages * page_size.
+ * read as zeros and raises device error bit 2; lengths are clipped to 0 .. max_pages * page_size, without
+ * an error bit (fp8_kv_pages_update, which makes them, reports those out of range).
  * Results do not depend on timing (parts of a shared request are added in a fixed order).
  * fp8q_check_attention_split (host only, host pointer): walks the division of the requests' tiles
  * over `workers` blocks with the kernel's own functions; 0 when every visible token is read exactly
