@@ -37,12 +37,12 @@
 // joined by a second launch in the blocks' order, so results do not depend on timing.
 //
 // Measured (us a call, calls back to back in a graph; HBM's floor at 6.53 TB/s):
-//   64 requests of 2000 .. 8192 tokens, 64 + 2 * 8 heads of 128    112.5 (102.6: 91 %)
-//   one request of 131072 tokens, a scale per token and head        56.5 (42.4)
-//   16 requests of 130 .. 4096 tokens, 32 + 2 * 8 heads of 128      21.5 (9.3)
-//   16 requests of up to 500 tokens, the same heads                  8.4 (1.4)
-//   one request of 33 tokens                                         4.5
-// The first runs at HBM's rate but for the 4 us before its first tile and the last blocks' end (345
+//   64 requests of 2000 .. 8192 tokens, 64 + 2 * 8 heads of 128    112.3 (102.6: 91 %)
+//   one request of 131072 tokens, a scale per token and head        57.1 (42.4)
+//   16 requests of 130 .. 4096 tokens, 32 + 2 * 8 heads of 128      21.7 (9.3)
+//   16 requests of up to 500 tokens, the same heads                  8.6 (1.7)
+//   one request of 33 tokens                                         4.4
+// The first runs at HBM's rate but for the 4 us before its first tile and the last blocks' end (350
 // instructions for 16 tokens of a head, 53 % of the issue slots); the shorter the work, the more its
 // fixed parts show: 4 us to the first tile (lengths, division, table, first copies), 1 us from the last
 // block's end to the second launch, 4 us of that.  Copies of whole tiles by the tensor unit (a box of 16
@@ -63,13 +63,14 @@ namespace attn {
 
 constexpr int kMaxWarps = 16;
 constexpr int kMaxWorkers = 1024;             // blocks of the first launch (one per SM)
-// least share of a block, in tiles (1: 11.4 us for one request of 1500 tokens against 10.6; 4: 11.1)
+// least share of a block, in tiles (one request of 1500 tokens: 10.7 us, with 4 11.3)
 constexpr int kMinTiles = 2;
-constexpr int kWholeTiles = 4;                // requests of fewer tiles a warp are not divided
+constexpr int kWholeTiles = 8;                // requests of no more tiles a warp are not divided (shape_of)
 constexpr int kSpreadRounds = 4;              // few requests of so many tiles a warp have their heads spread,
 constexpr int kSpreadPhases = 12;             // with so many warps a head at most (shape_of)
 constexpr int64_t kMaxCost = 0x7FFFFFFF;      // of all requests
-// a change of request, in tiles of a phase (16 ragged requests: 0 24.9 us, 1 23.2, 2 22.2, 3 21.6, 4 21.8)
+// a change of request, in tiles of a phase (us at 0 / 1 / 2 / 3 / 5: 16 ragged requests 24.8 23.2 22.1 21.7 22.0, 64
+// 113.7 112.5 112.0 112.2 113.2)
 constexpr int kTurn = 3;
 constexpr int kMaxTokens = 0x7FFFFFFF - 64;   // of one request: token numbers stay inside an int
 constexpr int kJoinWarps = 8;
@@ -1066,8 +1067,10 @@ inline Shape shape_of(int64_t batch, int64_t max_tokens, int heads, int group, i
   s.phases = warps / s.heads_per_block;
   const int64_t tiles = (max_tokens + kAttnTile - 1) / kAttnTile;
   // Requests that cannot have more than kWholeTiles tiles a warp stay with the block in whose share they
-  // begin, and there is no second launch.  us whole / divided (8 heads of 128, two warps each): 300 requests
-  // of up to 100 tokens 21.2 / 24.2, but one of 160 (5 tiles a warp) 10.4 / 9.5.
+  // begin, and there is no second launch.  us whole / divided, heads x dims: 300 requests of up to 100 tokens, 8 x 128,
+  // 22.3 / 25.2; of up to 250 33.5 / 34.5; 150 of up to 160 18.8 / 21.0, of up to 250 24.7 / 25.5, of up to 380 (12 tiles
+  // a warp) 31.6 / 29.0; 900 of up to 250 70.8 / 73.0; 4 x 256, 400 of up to 160 30.6 / 33.6; 16 x 128, 150 of up to 100
+  // 20.8 / 25.6.
   s.whole = tiles <= kWholeTiles * s.phases;
   // Where each request can have blocks of its own for one head or a few, its heads are spread over the machine
   // and it stays whole up to kSpreadRounds tiles of each of a head's warps: 48 tiles where a block has 16 warps,

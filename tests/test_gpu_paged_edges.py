@@ -169,6 +169,16 @@ def test_attention_wide_heads_spread(heads, group, d, most):
     attend(most + 1, [most], heads, group, d, 24, 1, 3, max_pages=-(-most // 24))
 
 
+@pytest.mark.parametrize("heads,most", [(16, 64), (16, 128), (16, 129), (8, 256), (8, 257), (5, 384), (5, 400)])
+@pytest.mark.parametrize("gran", [0, 3])
+def test_attention_many_short_requests(heads, most, gran):
+    """More requests than blocks, around the lengths up to which they stay whole."""
+    rng = np.random.default_rng(most)
+    lens = [int(n) for n in rng.integers(0, most + 1, 200)]
+    lens[7] = most
+    attend(heads, lens, heads, 1, 64, 16, 0, gran, max_pages=-(-most // 16))
+
+
 # ------------------------------------------------------------------ pages
 
 def update(table, lens, added, free, count, size, max_tokens):
