@@ -1044,9 +1044,9 @@ struct Shape {
 
 // head_dim is padded to 64, 128 or 256.  Groups above 8 query heads have two tiles of query rows a warp,
 // so a tile's codes are read and decoded once for both.  us with two tiles / with one: 64 requests of
-// up to 4096 tokens, 9 query heads a head of 128, 81 / 99; 16 requests, 16 a head of 128, 19.8 / 22.2; 64
-// requests, 12 a head of 256, 133 / 184; of one head of 256 in all, 16 a head, 7 requests 27.2 / 26.5 and
-// 64 of up to 16384 tokens 71 / 93.
+// up to 4096 tokens, 9 query heads a head of 128, 85 / 107, 12 a head of 64 54 / 68, 12 a head of 256 139 / 193;
+// 16 requests, 16 a head of 128, 30 / 36; of one head of 256 in all, 16 query heads, 7 requests 27.4 / 28.1 and
+// 64 of up to 16384 tokens 73 / 98.
 inline Shape shape_of(int64_t batch, int64_t max_tokens, int heads, int group, int head_dim) {
   Shape s;
   s.dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
@@ -1055,7 +1055,8 @@ inline Shape shape_of(int64_t batch, int64_t max_tokens, int heads, int group, i
   s.vheads = heads * s.row_tiles;
   const int warps = warps_of(s.dp, s.nh), sms = std::max(1, device_sm_count());
   // Heads are divided over the fewest groups of blocks; over more where that keeps a tenth more warps of
-  // the machine at work (5 of 8 warps with 5 heads of two row tiles, all of them with one head a block)
+  // the machine at work (5 of 8 warps with 5 heads of two row tiles, all of them with one head a block: 64
+  // requests of up to 4096 tokens 66 us against 81; 11 heads of 2 query heads 90 / 95)
   s.groups = (s.vheads + warps - 1) / warps;
   auto busy = [&](int groups) {              // warps at work, on average, of all SMs
     const int heads = (s.vheads + groups - 1) / groups;

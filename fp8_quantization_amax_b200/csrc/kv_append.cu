@@ -8,8 +8,8 @@
 // What bounds it: 2 bytes read an element and 2 (q) or 1 (k, v) written, against about ten
 // operations: HBM, once there are a few hundred tokens; below that the latency of one launch.
 // Measured (us a call, back to back in a graph; floor at 6.53 TB/s): 16384 tokens of 64 + 2 * 8 heads of
-// 128 without norm 112 (97.6: 87 %), 8192 tokens of 32 + 2 * 8 heads with norm and a scale per token
-// 39.1 (28.3: 72 %; 99 instructions for 256 elements, 46 % of the issue slots, the rest is waiting for
+// 128 without norm 111.7 (97.6: 87 %), 8192 tokens of 32 + 2 * 8 heads with norm and a scale per token
+// 38.8 (28.3: 73 %; 99 instructions for 256 elements, 46 % of the issue slots, the rest is waiting for
 // shuffles, shared memory and HBM at 24 warps an SM), 32 tokens 2.5.
 //
 // Angles: a frequency comes as a fraction of a turn in 64 bits, so position * frequency modulo one
@@ -415,8 +415,8 @@ cudaError_t launch(Params& p, cudaStream_t st) {
   p.block_tokens = (int)((p.tokens + room * waves - 1) / (room * waves));
   const unsigned x = (unsigned)((p.tokens + p.block_tokens - 1) / p.block_tokens);
   const unsigned y = (unsigned)std::min<int64_t>((units + warps - 1) / warps, std::max<int64_t>(1, room / p.tokens));
-  // rows rotated whole in halves: 36.4 us against 37.9 of the general form at 8192 tokens of 32 + 2 * 8 heads of
-  // 128; neighbouring pairs gain nothing (36.1 against 35.0)
+  // rows rotated whole in halves have fixed places: 36.4 us against 38.2 of the general form at 8192 tokens of
+  // 32 + 2 * 8 heads of 128 with norm, 32 tokens 2.5 / 2.7 (neighbouring pairs gained nothing by it, 36.1 / 35.0)
   if constexpr (!NEXT)
     if (p.c.head_dim == 16 * LPR && p.rot == p.c.head_dim)
       return launch_pdl(k_append<FMT, LPR, false, true>, dim3(x, y), dim3(32 * warps), 0, st, p);

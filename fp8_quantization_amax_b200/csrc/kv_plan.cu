@@ -17,7 +17,7 @@
 //
 // Measured (us a call, back to back in a graph): 256 decoding requests, 8 of which end, 5.9; prompts of 96
 // requests, 295 thousand tokens, 7.3 to 7.5 (the floor of the traffic is 0.6).  One launch against two: 6.5 /
-// 7.1 at 3100 tokens, 9.0 / 7.0 at 6200.
+// 6.9 at 3000 tokens of 8 requests, 7.6 / 6.8 at 4800, 11.6 / 7.0 at 9000.
 #include <cuda_runtime.h>
 
 #include <algorithm>
