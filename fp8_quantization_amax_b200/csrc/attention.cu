@@ -283,8 +283,20 @@ struct State {
   }
 };
 
+// ln(2^m l).  With scales of tokens m and log l may be far from 0 and cancel: l's exponent meets m first, or the
+// logarithm's error would be one of their size
+template <bool TOKEN_SCALES>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  if constexpr (TOKEN_SCALES) {
+    const uint32_t bits = __float_as_uint(l), exponent = bits >> 23;
+    if (exponent - 1u < 254u)                // neither 0, subnormal, infinite nor NaN
+      return kLn2 * ((m + (float)((int)exponent - 127)) + lg2(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u)));
+  }
+  return l == 0.0f ? -INFINITY : kLn2 * (m + lg2(l));
+}
+
 // out[b][head][dim] and lse of a finished state; vs: V's scale where it is one for the head
-template <int DP, int NH>
+template <int DP, int NH, bool TOKEN_SCALES>
 __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, int b, int vh, float vs, int lane) {
   constexpr int VB = DP / 8;
   const int g = lane >> 2, t = lane & 3;
@@ -298,8 +310,7 @@ __device__ __forceinline__ void write_rows(const Params& p, State<DP, NH>& s, in
       if (r >= p.group) continue;
       const float l = s.l[n][e], f = vs * (kDown * rcp(l));
       if (p.lse && g == 0)
-        p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] =
-            l == 0.0f ? -INFINITY : kLn2 * (s.m[n][e] + lg2(l));
+        p.lse[(int64_t)b * (p.c.heads * p.group) + kvh * p.group + r] = lse_of<TOKEN_SCALES>(s.m[n][e], l);
       uint16_t* dst = p.out + (int64_t)b * p.out_stride + (int64_t)(kvh * p.group + r) * D + g * VB;
 #pragma unroll
       for (int c = 0; c < VB / 8; ++c) {
@@ -879,7 +890,7 @@ __global__ void __launch_bounds__(32 * warps_of(DP, NH), 1) k_attention(const Pa
     const int place = c.left == t_end - t_begin ? 0 : 1;        // the block's first request, or a later one
     if (phase == 0) {
       if (opens && closes) {
-        write_rows<DP, NH>(p, s, c.b, vh, vscale, lane);
+        write_rows<DP, NH, TOKEN_SCALES>(p, s, c.b, vh, vscale, lane);
       } else {
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -1023,7 +1034,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_join(const Params p)
         const float l = r ? l1 : l0, m = r ? m1 : m0, f = vs * (kDown * rcp(l));
         const int64_t head = kvh * p.group + row + r;
         if (p.lse && tile == 0 && g == 0)
-          p.lse[(int64_t)e.x * (p.c.heads * p.group) + head] = l == 0.0f ? -INFINITY : kLn2 * (m + lg2(l));
+          p.lse[(int64_t)e.x * (p.c.heads * p.group) + head] = lse_of<TOKEN_SCALES>(m, l);
         if (dim < p.c.head_dim)
           *reinterpret_cast<uint32_t*>(p.out + (int64_t)e.x * p.out_stride + head * p.c.head_dim + dim) =
               f32x2_to_bf16x2(o[r] * f, o[2 + r] * f);

@@ -153,11 +153,15 @@ def test_attention_scales_of_either_sign(gran):
 @pytest.mark.parametrize("seed,lens,heads,group,d,size,fmt,gran,window,sinks,layout", [
     (251924, [9, 1, 9, 9, 1], 11, 9, 16, 5, 1, 3, 0, 0, "htd"),
     (238364, [1, 0, 5, 9, 9, 1], 33, 17, 16, 16, 0, 3, 0, 0, "thd"),
+    (833896, [1, 0, 2, 2, 1, 0, 2, 1, 2, 2, 1], 11, 17, 16, 16, 1, 2, 4, 15, "thd"),
+    (363082, [613, 1, 296, 289, 75, 613], 4, 24, 16, 128, 1, 2, 3, 16, "htd"),
+    (967120, [1] * 24, 8, 16, 16, 128, 1, 3, 0, 0, "thd"),
     (7, [1] * 40, 16, 1, 48, 32, 1, 2, 0, 0, "htd"),
     (8, list(range(60)), 16, 3, 48, 16, 1, 3, 8, 17, "thd"),
 ])
 def test_attention_lse_of_few_tokens(seed, lens, heads, group, d, size, fmt, gran, window, sinks, layout):
-    """The sum of few weights near 1 is what their logarithm is taken of: factors for f16 do not enter it."""
+    """The sum of few weights near 1 is what their logarithm is taken of: factors for f16 do not enter it, and a
+    sum far from 1 (V's scales of tokens are in the reference) meets the reference before the logarithm."""
     attend(seed, lens, heads, group, d, size, fmt, gran, window, sinks, layout)
 
 
