@@ -246,7 +246,10 @@ __global__ void __launch_bounds__(kChunk) k_pages_plan(const Params p) {
     for (uint32_t i0 = tid; i0 < most; i0 += kCopies * kChunk) {
       int page[kCopies];                     // in flight together
 #pragma unroll
-      for (int c = 0; c < kCopies; ++c) page[c] = i0 + c * kChunk < most ? back_page(p.table, p.max_pages, first, ending, givers, i0 + c * kChunk) : 0;
+      for (int c = 0; c < kCopies; ++c) {
+        const uint32_t i = i0 + c * kChunk;
+        page[c] = i < most ? back_page(p.table, p.max_pages, first, ending, givers, (int)i) : 0;
+      }
 #pragma unroll
       for (int c = 0; c < kCopies; ++c) {
         marked |= page[c] < 0;

@@ -624,7 +624,9 @@ FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_pages *cache, const void *q, in
  * Attention of one new token per request over its pages:
  *   z_j = scale * s_k(j) * sum_d q[d] decode(K_j[d]),  out = sum_j softmax(z)_j s_v(j) decode(V_j)
  * for each query head over the request's visible tokens; q_heads / heads query heads share a
- * key-value head.  Sums and softmax in fp32, the softmax weights rounded to f16 for the product.
+ * key-value head.  Sums and softmax in fp32, the softmax weights rounded to f16 for the product: by 2^-11
+ * of a weight, or 2^-34 of the row's largest (with scales of tokens: weight times V's scale, one below
+ * 2^-60 counting as that) where that is more.
  *   q             bf16 [batch][q_heads][head_dim], requests q_stride elements apart
  *   block_table   int32 [batch][max_pages], lens int32 [batch]: as fp8_kv_pages_update leaves them;
  *                 lens counts the new token (append it first)
